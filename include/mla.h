@@ -43,6 +43,18 @@
  *     [page_size][d_rope] bf16 k^R, then [page_size][d_c/128] fp32 scales;
  *     c[j] = e4m3(code[j]) * scale[j/128], scale = amax of the 128-wide tile
  *     / 448 (1 for an all-zero tile).  Sub-blocks start at multiples of 128 B.
+ *   MLA_FP4_E2M1 cache: page = [page_size][d_c/2] bytes of e2m1 code pairs
+ *     (element 2i in the low four bits of byte i), then [page_size][d_rope]
+ *     bf16 k^R, then [page_size][d_c/16] e4m3 block scales s, then [page_size]
+ *     fp32 token scales ts; c[j] = e2m1(code[j]) * s[j/16] * ts.  ts is a power
+ *     of two: with a = max(max|c|, max|k^R| / 64) over the token (k^R as
+ *     stored), ts = 2^(floor(log2 a) - 5), at least 2^-100, and 1 where a = 0.
+ *     s = e4m3(max|block| / (6 ts)) and code = e2m1(c / (s ts)), fp32
+ *     quotients, round to nearest even, saturating; code 0 where s = 0.  A
+ *     value has at most six significant bits, so it is exact in bf16.  A
+ *     non-finite element takes no part in the maxima and sets its block's s to
+ *     the e4m3 NaN (its 16 elements read as NaN).  Sub-blocks start at
+ *     multiples of 128 B.  DeepSeek-V3 dims: 420 B per token.
  *   mla_cache_page_bytes() gives the page size in bytes.
  *   Token `pos` of sequence b lives in row pos % page_size of physical page
  *   page_table[b * max_pages + pos / page_size].
@@ -57,7 +69,7 @@
 extern "C" {
 #endif
 
-typedef enum { MLA_F32 = 0, MLA_BF16 = 1, MLA_FP8_E4M3 = 2 } mla_dtype;
+typedef enum { MLA_F32 = 0, MLA_BF16 = 1, MLA_FP8_E4M3 = 2, MLA_FP4_E2M1 = 3 } mla_dtype;
 
 enum {
   MLA_OK = 0,
@@ -104,7 +116,7 @@ typedef struct {
   int32_t d_model;     /* model width d (7168); multiple of 8 */
   int32_t page_size;   /* tokens per cache page (64) */
   int32_t act_dtype;   /* mla_dtype: MLA_F32 or MLA_BF16 */
-  int32_t cache_dtype; /* mla_dtype: MLA_F32 (needs act F32), MLA_BF16 or MLA_FP8_E4M3 (need act BF16) */
+  int32_t cache_dtype; /* mla_dtype: MLA_F32 (needs act F32), MLA_BF16, MLA_FP8_E4M3 or MLA_FP4_E2M1 */
   float softmax_scale; /* 1/sqrt(d_nope + d_rope) in the pages' module */
   float rope_base;     /* 10000 */
   uint32_t flags;      /* MLA_FLAG_* */
@@ -131,8 +143,8 @@ int mla_check_dims(const mla_dims* dims);
  *   page_table [batch, max_pages] int32
  *   cache_pool num_pages pages (layout above), written
  *   workspace  >= mla_append_workspace_bytes(dims, n_tokens) bytes of scratch
- *              (fp32 c values between the projection and the FP8 quantiser;
- *              0 bytes, and workspace may be NULL, for fp32/bf16 caches).
+ *              (fp32 c values between the projection and the FP8 or 4-bit
+ *              quantiser; 0 bytes, and workspace may be NULL, for fp32/bf16 caches).
  *              With >= mla_append_workspace_bytes_fast(dims, n_tokens) bytes
  *              (16-byte aligned), a step of 16 to 511 tokens at DeepSeek-V3
  *              dims with bf16 activations takes the split-K tensor-core
@@ -158,8 +170,8 @@ size_t mla_append_workspace_bytes_fast(const mla_dims* dims, int n_tokens);
  * fp32 scratch lives in a fixed array inside the library, 65,536 floats
  * (256 KiB) on every GPU that loads it, held until the process exits.
  *   - The scratch a call uses is what mla_append_workspace_bytes() reports:
- *     n_tokens * d_c floats for an FP8 cache, none for bf16 and fp32 caches.
- *     An FP8 request must fit the array (n_tokens * d_c <= 65536: 128 tokens
+ *     n_tokens * d_c floats for an FP8 or 4-bit cache, none for bf16 and fp32
+ *     caches.  An FP8 or 4-bit request must fit the array (n_tokens * d_c <= 65536: 128 tokens
  *     at DeepSeek-V3 dims); a larger one returns MLA_ERR_WORKSPACE and
  *     launches nothing.  bf16 and fp32 caches have no size limit here.
  *   - The first call on a device looks up the array's device address (with
@@ -179,6 +191,52 @@ int mla_append_latent(const mla_dims* dims, const void* h, int n_tokens,
                       const int32_t* page_table, int batch, int max_pages,
                       void* cache_pool, int num_pages,
                       void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * mla_append_rows: write cache rows whose projection the caller has done (a
+ * fused down-projection that yields [c | k^R] beside other outputs, or one with
+ * a norm before the cache).  The articles' append projects inside; this is its
+ * store alone, with the RMSNorm of the latent that models put in between.
+ *   c~_n  = c_n, or with norm_weight  norm_weight * c_n / sqrt(mean(c_n^2) + norm_eps)
+ *   k^R_n = RoPE(k_rope_n, pos[n])   (as mla_append_latent)
+ * and store [c~_n | k^R_n] at (seq_idx[n], pos[n]), rounded once to the cache
+ * type (the quantisers of the layouts above, from the fp32 value of c~).
+ *   c           n_tokens rows of d_c act elements, c_stride elements apart
+ *   k_rope      n_tokens rows of d_rope act elements, k_stride elements apart,
+ *               not rotated; may be NULL when d_rope is 0
+ *   norm_weight [d_c] act, or NULL for no norm; norm_eps > 0 with it
+ *   seq_idx, pos, page_table, batch, max_pages, cache_pool, num_pages as for
+ *               mla_append_latent
+ * Rows need no alignment beyond their type's; 16-byte aligned c and
+ * norm_weight with a c_stride of whole 16 bytes take the faster accesses, with
+ * the same results.  No workspace.  Out-of-range seq_idx/pos/page entries: the
+ * token is skipped and MLA_ERR_BOUNDS is recorded.  Each (seq_idx, pos) may
+ * occur once in a call (of two, the row is undefined).  No byte outside the
+ * tokens' rows changes.  n_tokens == 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+int mla_append_rows(const mla_dims* dims, const void* c, int64_t c_stride,
+                    const void* k_rope, int64_t k_stride, const void* norm_weight,
+                    float norm_eps, int n_tokens, const int32_t* seq_idx,
+                    const int32_t* pos, const int32_t* page_table, int batch,
+                    int max_pages, void* cache_pool, int num_pages, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * mla_read_rows: cache rows back as values, for callers that attend, check or
+ * export outside this library.
+ *   c_out [n_tokens, d_c] act: the latent of (seq_idx[n], pos[n]), dequantised
+ *         in fp32 and rounded once to the act type (exact for bf16 and 4-bit
+ *         caches)
+ *   k_out [n_tokens, d_rope] act: the stored (rotated) k^R; may be NULL when
+ *         d_rope is 0
+ * A position may be read more than once, and none has to be below a sequence
+ * length: what the row holds is returned.  Out-of-range seq_idx/pos/page
+ * entries: the token's output rows are left as they were and MLA_ERR_BOUNDS is
+ * recorded.  n_tokens == 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+int mla_read_rows(const mla_dims* dims, const void* cache_pool, int num_pages,
+                  const int32_t* page_table, int batch, int max_pages,
+                  const int32_t* seq_idx, const int32_t* pos, int n_tokens,
+                  void* c_out, void* k_out, void* stream);
 
 /* ---------------------------------------------------------------------------
  * S2+S3  mla_decode: absorb the queries and run split-KV attention over the
@@ -250,7 +308,8 @@ int mla_combine(const mla_dims* dims, const void* W_uv, int batch, int n_q, int 
  *   out [batch, n_q, n_heads, d_v] act, lse_out [batch, n_q, n_heads] float32
  *   natural-log softmax denominators (may be NULL)
  * DeepSeek-V3 dims only (d_c 512, d_rope 64, d_nope = d_v = 128, 64-token
- * pages), bf16 activations, bf16 or FP8 cache; MLA_ERR_UNSUPPORTED otherwise.
+ * pages), bf16 activations, bf16, FP8 or 4-bit cache; MLA_ERR_UNSUPPORTED
+ * otherwise.
  * ------------------------------------------------------------------------- */
 size_t mla_prefill_workspace_bytes(const mla_dims* dims, int max_seq_len);
 int mla_prefill(const mla_dims* dims, const void* q_nope, const void* q_rope,
@@ -269,7 +328,7 @@ int mla_auto_splits(const mla_dims* dims, int batch, int n_q);
 /* Tracing.  Kernels of the calls above, in launch order per step: */
 enum {
   MLA_TRACE_APPEND_PROJECT = 0, /* mla_append_latent: [W_dkv; W_kr] h, RoPE, paged store */
-  MLA_TRACE_APPEND_FINALIZE = 1,/* mla_append_latent: FP8 quantiser (FP8 caches only) */
+  MLA_TRACE_APPEND_FINALIZE = 1,/* mla_append_latent: FP8 or 4-bit quantiser; mla_append_rows: its kernel */
   MLA_TRACE_ABSORB = 2,         /* mla_decode: q~ = W_uk^T q_nope, RoPE(q_rope), split plan */
   MLA_TRACE_ATTEND = 3,         /* mla_decode: split-KV attention over the cache */
   MLA_TRACE_COMBINE = 4,        /* mla_combine: split merge and W_uv */

@@ -14,7 +14,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmla.so")
 
-MLA_F32, MLA_BF16, MLA_FP8_E4M3 = 0, 1, 2
+MLA_F32, MLA_BF16, MLA_FP8_E4M3, MLA_FP4_E2M1 = 0, 1, 2, 3
 MLA_FLAG_FORCE_SIMT = 1
 MLA_FLAG_SELFTEST_STALL = 2  # decode issues no loads, combine no weight fetch: bounded waits expire (tests)
 
@@ -27,7 +27,7 @@ ERRORS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "M
 # Every entry point declared in include/mla.h.
 EXPORTED = ("mla_cache_page_bytes", "mla_check_dims", "mla_append_workspace_bytes",
             "mla_append_workspace_bytes_fast", "mla_append_latent",
-            "mla_append_latent_noalloc",
+            "mla_append_latent_noalloc", "mla_append_rows", "mla_read_rows",
             "mla_decode_workspace_bytes", "mla_decode", "mla_combine", "mla_prefill_workspace_bytes",
             "mla_prefill", "mla_decode_path", "mla_auto_splits",
             "mla_set_trace_events", "mla_set_timeline", "mla_get_status", "mla_error_string")
@@ -66,6 +66,11 @@ def lib() -> ctypes.CDLL:
         L.mla_append_latent.restype = I
         L.mla_append_latent_noalloc.argtypes = [S, P, I, P, P, P, P, P, I, I, P, I, P]
         L.mla_append_latent_noalloc.restype = I
+        Q = ctypes.c_int64
+        L.mla_append_rows.argtypes = [S, P, Q, P, Q, P, ctypes.c_float, I, P, P, P, I, I, P, I, P]
+        L.mla_append_rows.restype = I
+        L.mla_read_rows.argtypes = [S, P, I, P, I, I, P, P, I, P, P, P]
+        L.mla_read_rows.restype = I
         L.mla_decode_workspace_bytes.argtypes, L.mla_decode_workspace_bytes.restype = [S, I, I, I], Z
         L.mla_decode.argtypes = [S, P, P, P, P, I, P, I, P, I, I, I, P, Z, P]
         L.mla_decode.restype = I
@@ -90,7 +95,7 @@ def error_string(code: int) -> str:
 
 def make_dims(n_heads, d_c, d_rope, d_nope, d_v, d_model, page_size=64, act="bf16", cache="bf16",
               softmax_scale=None, rope_base=10000.0, flags=0) -> MlaDims:
-    codes = {"f32": MLA_F32, "bf16": MLA_BF16, "fp8": MLA_FP8_E4M3}
+    codes = {"f32": MLA_F32, "bf16": MLA_BF16, "fp8": MLA_FP8_E4M3, "fp4": MLA_FP4_E2M1}
     if softmax_scale is None:
         softmax_scale = (d_nope + d_rope) ** -0.5
     return MlaDims(n_heads, d_c, d_rope, d_nope, d_v, d_model, page_size, codes[act], codes[cache],
@@ -175,6 +180,60 @@ def mla_append_latent_noalloc(dims, h, seq_idx, pos, W_dkv, W_kr, page_table, ca
                                          _ptr(W_dkv), _ptr(W_kr), _ptr(page_table), page_table.shape[0],
                                          page_table.shape[1], _ptr(cache_pool), num_pages, _stream(stream))
     _check(rc, "mla_append_latent_noalloc")
+
+
+def _rows(x, width, what):
+    """Row stride (elements) of a [N, width] CUDA tensor with contiguous rows."""
+    if x.dim() != 2 or x.shape[1] != width or not x.is_cuda or (width > 1 and x.shape[0] > 0 and x.stride(1) != 1):
+        raise ValueError(f"{what}: a CUDA tensor [N, {width}] with contiguous rows")
+    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), width)
+
+
+def _index(n, *ts):
+    for t in ts:
+        if t.dtype != torch.int32 or t.numel() != n:
+            raise ValueError("seq_idx and pos: one int32 per row")
+
+
+def act_dtype(dims: MlaDims):
+    return torch.float32 if dims.act_dtype == MLA_F32 else torch.bfloat16
+
+
+def mla_append_rows(dims, c, k_rope, seq_idx, pos, page_table, cache_pool, norm_weight=None, norm_eps=1e-6,
+                    stream=None):
+    """Append already projected rows: c [N, d_c] (RMSNorm with norm_weight [d_c]
+    if given) and k_rope [N, d_rope] (not rotated), both views with contiguous
+    rows (a slice of a fused projection's output serves), go to
+    (seq_idx[n], pos[n]) of the paged cache."""
+    _cuda(seq_idx, pos, page_table, cache_pool, norm_weight)
+    n, act = c.shape[0], act_dtype(dims)
+    cs, ks = _rows(c, dims.d_c, "c"), _rows(k_rope, dims.d_rope, "k_rope")
+    if k_rope.shape[0] != n:
+        raise ValueError("c and k_rope: the same number of rows")
+    if c.dtype != act or k_rope.dtype != act or (norm_weight is not None and
+                                                 (norm_weight.dtype != act or norm_weight.numel() != dims.d_c)):
+        raise ValueError(f"c, k_rope and norm_weight [d_c]: {act}")
+    _index(n, seq_idx, pos)
+    num_pages = cache_pool.numel() * cache_pool.element_size() // cache_page_bytes(dims)
+    rc = lib().mla_append_rows(ctypes.byref(dims), _ptr(c), cs, _ptr(k_rope), ks, _ptr(norm_weight), norm_eps, n,
+                               _ptr(seq_idx), _ptr(pos), _ptr(page_table), page_table.shape[0], page_table.shape[1],
+                               _ptr(cache_pool), num_pages, _stream(stream))
+    _check(rc, "mla_append_rows")
+
+
+def mla_read_rows(dims, cache_pool, page_table, seq_idx, pos, c_out, k_out, stream=None):
+    """Cache rows (seq_idx[n], pos[n]) back as values: c_out [N, d_c], k_out [N, d_rope]."""
+    _cuda(cache_pool, page_table, seq_idx, pos, c_out, k_out)
+    n, act = seq_idx.numel(), act_dtype(dims)
+    if tuple(c_out.shape) != (n, dims.d_c) or tuple(k_out.shape) != (n, dims.d_rope) or c_out.dtype != act or \
+            k_out.dtype != act:
+        raise ValueError(f"c_out [N, d_c], k_out [N, d_rope]: {act}")
+    _index(n, seq_idx, pos)
+    num_pages = cache_pool.numel() * cache_pool.element_size() // cache_page_bytes(dims)
+    rc = lib().mla_read_rows(ctypes.byref(dims), _ptr(cache_pool), num_pages, _ptr(page_table), page_table.shape[0],
+                             page_table.shape[1], _ptr(seq_idx), _ptr(pos), n, _ptr(c_out), _ptr(k_out),
+                             _stream(stream))
+    _check(rc, "mla_read_rows")
 
 
 def mla_decode(dims, q_nope, q_rope, W_uk, cache_pool, page_table, seq_lens, workspace, num_splits=0,

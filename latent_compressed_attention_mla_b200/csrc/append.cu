@@ -24,7 +24,8 @@
 //   d_rope/2) in columns (j, j + 16), so RoPE stays inside a tile.
 // append_fp8_finalize: FP8 caches need the amax of each 128-wide tile of c, a
 //   reduction across CTAs, so the projection leaves c in fp32 scratch and one
-//   CTA per token quantises it.
+//   CTA per token quantises it.  4-bit caches run the same projections and
+//   their own quantiser (append_fp4_finalize, rows.cu).
 #include <cooperative_groups.h>
 #include <cuda.h>
 
@@ -56,7 +57,8 @@ struct AppendArgs {
   size_t page_bytes;
   int d_c, d_rope, d_model, page_size;
   float rope_base;
-  float* raw;  // fp32 [n_tokens][d_c] scratch (FP8 caches only)
+  float* raw;  // fp32 [n_tokens][d_c] scratch (quantised caches only)
+  size_t kr_off;  // k^R rows in a page of a quantised cache
   int* status;
   unsigned long long* timeline;  // device timeline (null: off)
 };
@@ -95,7 +97,7 @@ struct AppendGemm {
   int trace;
   int stall;
   AppendArgs a;
-  int fp8;
+  int coded;           // FP8 or 4-bit cache: c to the fp32 scratch, k^R to the page's bf16 block
   CUtensorMap map_h;   // h [n_tokens][d_model], box 64 x 128 (rows past n_tokens read as zero)
   CUtensorMap map_wd;  // W_dkv [512][d_model], box 64 x 64
   CUtensorMap map_wk;  // W_kr [64][d_model], box 64 x 64
@@ -127,7 +129,7 @@ struct AppendGemm {
       tc_ld32(taddr + 32 * c4, v);  // whole-warp: every lane loads, live or not
       if (!pg) continue;
       const int col = kAgN * nt + 32 * c4;
-      if (fp8) {
+      if (coded) {
         float4* dst = reinterpret_cast<float4*>(a.raw + (size_t)n * 512 + col);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
@@ -148,10 +150,9 @@ struct AppendGemm {
     if (nt != 2) return;
     // k^R: pair (i, i + 32) rotated by the angle of the token's position; one
     // TMEM column of each at a time keeps the rolled loop in registers
-    const Fp8Page fp = fp8_page(a.page_size, 512, 64);
     __nv_bfloat16* kr = !pg ? nullptr
-                        : fp8 ? reinterpret_cast<__nv_bfloat16*>(pg + fp.kr_off) + (size_t)prow * 64
-                              : reinterpret_cast<__nv_bfloat16*>(pg) + (size_t)prow * 576 + 512;
+                        : coded ? reinterpret_cast<__nv_bfloat16*>(pg + a.kr_off) + (size_t)prow * 64
+                                : reinterpret_cast<__nv_bfloat16*>(pg) + (size_t)prow * 576 + 512;
 #pragma unroll 1
     for (int i = 0; i < 32; ++i) {
       const float x1 = __uint_as_float(tc_ld1(taddr + 128 + i)), x2 = __uint_as_float(tc_ld1(taddr + 160 + i));
@@ -202,7 +203,7 @@ constexpr int kAsMaxSplits = 16;      // and at most this many partials per outp
 // Splits of a split-K append of n tokens at these dims, or 0 when that path
 // does not apply.
 int append_splitk_splits(const mla_dims& d, int n_tokens) {
-  if (d.act_dtype != MLA_BF16 || (d.cache_dtype != MLA_BF16 && d.cache_dtype != MLA_FP8_E4M3) || d.d_c != 512 ||
+  if (d.act_dtype != MLA_BF16 || (d.cache_dtype != MLA_BF16 && !is_coded_cache(d)) || d.d_c != 512 ||
       d.d_rope != 64 || d.d_model % 64 != 0 || n_tokens < kAsMinTokens || n_tokens >= kAgMinTokens)
     return 0;
   const int m_tiles = (n_tokens + 127) / 128, k_chunks = d.d_model / 64;
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(288) append_splitk_finish_kernel(const AppendA
   pdl_wait();
   tl_begin(a.timeline, MLA_TRACE_APPEND_FINALIZE);
   __shared__ int s_slot[3];
-  __shared__ float s_max[8];
+  __shared__ float s_max[9];
   const int n = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     int prow = 0, position = 0;
@@ -289,6 +290,38 @@ __global__ void __launch_bounds__(288) append_splitk_finish_kernel(const AppendA
   }
   const Fp8Page fp = fp8_page(a.page_size, 512, 64);
   float scale = 1.f;
+  // k^R before the scales: a 4-bit row's token scale looks at it too
+  float y0 = 0.f, y1 = 0.f;
+  if (tid >= 256) {
+    float cs, sn;
+    rope_cos_sin(position, i, 32, a.rope_base, &cs, &sn);
+    y0 = x0 * cs - x1 * sn;
+    y1 = x1 * cs + x0 * sn;
+  }
+  float ts = 1.f, amax16 = 0.f;
+  bool finite = true;
+  if (CACHE == MLA_FP4_E2M1) {
+    // threads 8 k .. 8 k + 7 hold block k of 16 columns; the token's maxima of
+    // c (warps 0-7) and of the bf16 k^R (warp 8) meet in shared memory
+    bool kr_ok = true;
+    float m = tid < 256 ? fmaxf(finite_abs(x0, finite), finite_abs(x1, finite))
+                        : fmaxf(finite_abs(__bfloat162float(__float2bfloat16_rn(y0)), kr_ok),
+                                finite_abs(__bfloat162float(__float2bfloat16_rn(y1)), kr_ok));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      finite = __shfl_xor_sync(0xffffffffu, (int)finite, o) != 0 && finite;
+    }
+    amax16 = m;
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    float c_max = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) c_max = fmaxf(c_max, s_max[q]);
+    ts = fp4_token_scale(c_max, s_max[8]);
+  }
   if (CACHE == MLA_FP8_E4M3) {
     // per 128-column tile of c (threads 64 t .. 64 t + 63: warps 2 t, 2 t + 1):
     // scale = amax / 448 (IEEE fp32 division; 1 for an all-zero tile)
@@ -309,16 +342,20 @@ __global__ void __launch_bounds__(288) append_splitk_finish_kernel(const AppendA
         const uint32_t hi = __nv_cvt_float_to_fp8(x1 / scale, __NV_SATFINITE, __NV_E4M3);
         *reinterpret_cast<uint16_t*>(pg + (size_t)prow * 512 + 2 * tid) = (uint16_t)(lo | (hi << 8));
         if ((tid & 63) == 0) reinterpret_cast<float*>(pg + fp.sc_off)[(size_t)prow * 4 + (tid >> 6)] = scale;
+      } else if (CACHE == MLA_FP4_E2M1) {
+        const Fp4Page f4 = fp4_page(a.page_size, 512, 64);
+        const uint32_t sc = fp4_block_scale(amax16, ts, finite);
+        pg[(size_t)prow * 256 + tid] = (uint8_t)fp4_pair(x0, x1, e4m3_to_float((uint8_t)sc) * ts);
+        if ((tid & 7) == 0) pg[f4.sc_off + (size_t)prow * 32 + (tid >> 3)] = (uint8_t)sc;
+        if (tid == 0) reinterpret_cast<float*>(pg + f4.ts_off)[prow] = ts;
       } else {
         *reinterpret_cast<__nv_bfloat162*>(pg + ((size_t)prow * 576 + 2 * tid) * 2) = __floats2bfloat162_rn(x0, x1);
       }
     } else {
-      float cs, sn;
-      rope_cos_sin(position, i, 32, a.rope_base, &cs, &sn);
-      __nv_bfloat16* kr = CACHE == MLA_FP8_E4M3 ? reinterpret_cast<__nv_bfloat16*>(pg + fp.kr_off) + (size_t)prow * 64
-                                                : reinterpret_cast<__nv_bfloat16*>(pg) + (size_t)prow * 576 + 512;
-      kr[i] = __float2bfloat16_rn(x0 * cs - x1 * sn);
-      kr[i + 32] = __float2bfloat16_rn(x1 * cs + x0 * sn);
+      __nv_bfloat16* kr = CACHE != MLA_BF16 ? reinterpret_cast<__nv_bfloat16*>(pg + a.kr_off) + (size_t)prow * 64
+                                            : reinterpret_cast<__nv_bfloat16*>(pg) + (size_t)prow * 576 + 512;
+      kr[i] = __float2bfloat16_rn(y0);
+      kr[i + 32] = __float2bfloat16_rn(y1);
     }
   }
   tl_end(a.timeline, MLA_TRACE_APPEND_FINALIZE);
@@ -411,8 +448,7 @@ __global__ void __launch_bounds__(256, 2) append_project_kernel(const AppendArgs
               rope_cos_sin(position, i, half, a.rope_base, &cs, &sn);
               const float y1 = x1 * cs - x2 * sn, y2 = x2 * cs + x1 * sn;
               if (CACHE == MLA_FP8_E4M3) {
-                const Fp8Page fp = fp8_page(a.page_size, a.d_c, a.d_rope);
-                __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(pg + fp.kr_off) + (size_t)prow * a.d_rope;
+                __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(pg + a.kr_off) + (size_t)prow * a.d_rope;
                 kr[i] = __float2bfloat16_rn(y1);
                 kr[i + half] = __float2bfloat16_rn(y2);
               } else {
@@ -556,8 +592,7 @@ __global__ void __launch_bounds__(kGvThreads) append_gemv_kernel(const AppendArg
         uint8_t* pg = a.pool + (size_t)page * a.page_bytes;
         __nv_bfloat16* kr;
         if (CACHE == MLA_FP8_E4M3) {
-          const Fp8Page fp = fp8_page(a.page_size, a.d_c, a.d_rope);
-          kr = reinterpret_cast<__nv_bfloat16*>(pg + fp.kr_off) + (size_t)s_row[n_tok] * a.d_rope;
+          kr = reinterpret_cast<__nv_bfloat16*>(pg + a.kr_off) + (size_t)s_row[n_tok] * a.d_rope;
         } else {
           kr = reinterpret_cast<__nv_bfloat16*>(pg) + (size_t)s_row[n_tok] * (a.d_c + a.d_rope) + a.d_c;
         }
@@ -673,7 +708,6 @@ __global__ void __cluster_dims__(kTcCluster, 1, 1) __launch_bounds__(kTcThreads,
   pdl_wait();
   MLA_STAMP(1);
   tl_begin(a.timeline, MLA_TRACE_APPEND_PROJECT);
-  const Fp8Page fp = fp8_page(a.page_size, a.d_c, a.d_rope);
   const int M = a.n_tokens, nk = ks / 16;
   uint32_t pass = 0;
   for (int m0 = 0; m0 < M; m0 += kTcMb, ++pass) {
@@ -757,7 +791,7 @@ __global__ void __cluster_dims__(kTcCluster, 1, 1) __launch_bounds__(kTcThreads,
         rope_cos_sin(position, i, half, a.rope_base, &cs, &sn);
         const float y1 = v0 * cs - v1 * sn, y2 = v1 * cs + v0 * sn;
         __nv_bfloat16* kr = CACHE == MLA_FP8_E4M3
-                                ? reinterpret_cast<__nv_bfloat16*>(pg + fp.kr_off) + (size_t)prow * a.d_rope
+                                ? reinterpret_cast<__nv_bfloat16*>(pg + a.kr_off) + (size_t)prow * a.d_rope
                                 : reinterpret_cast<__nv_bfloat16*>(pg) + (size_t)prow * (a.d_c + a.d_rope) + a.d_c;
         kr[i] = __float2bfloat16_rn(y1);
         kr[i + half] = __float2bfloat16_rn(y2);
@@ -776,6 +810,7 @@ size_t cache_page_bytes(const mla_dims& d) {
   const size_t D = (size_t)d.d_c + d.d_rope;
   if (d.cache_dtype == MLA_F32) return (size_t)d.page_size * D * 4;
   if (d.cache_dtype == MLA_BF16) return (size_t)d.page_size * D * 2;
+  if (d.cache_dtype == MLA_FP4_E2M1) return fp4_page(d.page_size, d.d_c, d.d_rope).bytes;
   const Fp8Page fp = fp8_page(d.page_size, d.d_c, d.d_rope);
   return a128(fp.sc_off + (size_t)d.page_size * (d.d_c / 128) * 4);
 }
@@ -790,7 +825,7 @@ size_t append_splitk_floats(const mla_dims& d, int n_tokens) {
 }
 
 size_t append_scratch_floats(const mla_dims& d, int n_tokens) {
-  return d.cache_dtype == MLA_FP8_E4M3 ? (size_t)n_tokens * d.d_c : 0;
+  return is_coded_cache(d) ? (size_t)n_tokens * d.d_c : 0;
 }
 
 cudaError_t launch_append(const mla_dims& d, const void* h, int n_tokens, const int32_t* seq_idx,
@@ -817,6 +852,7 @@ cudaError_t launch_append(const mla_dims& d, const void* h, int n_tokens, const 
   a.page_size = d.page_size;
   a.rope_base = d.rope_base;
   a.raw = raw;
+  a.kr_off = coded_kr_off(d.cache_dtype, d.page_size, d.d_c, d.d_rope);
   a.status = status;
   a.timeline = timeline_ptr();
   const int grid = (d.d_c + kRows - 1) / kRows + d.d_rope / 2;
@@ -828,7 +864,10 @@ cudaError_t launch_append(const mla_dims& d, const void* h, int n_tokens, const 
                     d.d_model % 8 == 0 && d.d_model <= kGvThreads * kGvVec * 8 && d.d_c % kGvCols == 0 &&
                     d.d_rope % kGvCols == 0 && (reinterpret_cast<uintptr_t>(h) & 15u) == 0 &&
                     (reinterpret_cast<uintptr_t>(W_dkv) & 15u) == 0 && (reinterpret_cast<uintptr_t>(W_kr) & 15u) == 0;
-  const bool big = d.act_dtype == MLA_BF16 && (d.cache_dtype == MLA_BF16 || d.cache_dtype == MLA_FP8_E4M3) &&
+  // A 4-bit cache runs the FP8 cache's projection kernels: they leave c in the
+  // fp32 scratch and k^R at kr_off, and only the quantiser that follows differs.
+  const bool coded = is_coded_cache(d);
+  const bool big = d.act_dtype == MLA_BF16 && (d.cache_dtype == MLA_BF16 || coded) &&
                    d.d_c == 512 && d.d_rope == 64 && d.d_model % 64 == 0 && n_tokens >= kAgMinTokens &&
                    (reinterpret_cast<uintptr_t>(h) & 15u) == 0 && (reinterpret_cast<uintptr_t>(W_dkv) & 15u) == 0 &&
                    (reinterpret_cast<uintptr_t>(W_kr) & 15u) == 0;
@@ -864,14 +903,13 @@ cudaError_t launch_append(const mla_dims& d, const void* h, int n_tokens, const 
     if (launch_err == cudaSuccess) launch_err = cudaGetLastError();
     trace_record(MLA_TRACE_APPEND_PROJECT, true, st);
     if (launch_err != cudaSuccess) return launch_err;
-    // the partials -> the cache rows (bf16, or the FP8 quantiser)
+    // the partials -> the cache rows (bf16, or the quantised cache's codes)
     trace_record(MLA_TRACE_APPEND_FINALIZE, false, st);
     const int rows_pad = 128 * g.m_tiles;
-    launch_err = d.cache_dtype == MLA_FP8_E4M3
-                     ? launch_pdl(append_splitk_finish_kernel<MLA_FP8_E4M3>, dim3(n_tokens), dim3(288), 0, st, a,
-                                  (const float*)raw, g.splits, rows_pad)
-                     : launch_pdl(append_splitk_finish_kernel<MLA_BF16>, dim3(n_tokens), dim3(288), 0, st, a,
-                                  (const float*)raw, g.splits, rows_pad);
+    auto finish = d.cache_dtype == MLA_FP8_E4M3   ? append_splitk_finish_kernel<MLA_FP8_E4M3>
+                  : d.cache_dtype == MLA_FP4_E2M1 ? append_splitk_finish_kernel<MLA_FP4_E2M1>
+                                                  : append_splitk_finish_kernel<MLA_BF16>;
+    launch_err = launch_pdl(finish, dim3(n_tokens), dim3(288), 0, st, a, (const float*)raw, g.splits, rows_pad);
     if (launch_err == cudaSuccess) launch_err = cudaGetLastError();
     trace_record(MLA_TRACE_APPEND_FINALIZE, true, st);
     return launch_err;
@@ -879,7 +917,7 @@ cudaError_t launch_append(const mla_dims& d, const void* h, int n_tokens, const 
     AppendGemm g;
     memset(&g, 0, sizeof(g));
     g.a = a;
-    g.fp8 = d.cache_dtype == MLA_FP8_E4M3;
+    g.coded = coded;
     g.tiles = (n_tokens + 127) / 128 * 3;
     g.k_chunks = d.d_model / 64;
     g.status = status;
@@ -899,7 +937,7 @@ cudaError_t launch_append(const mla_dims& d, const void* h, int n_tokens, const 
                               dim3(kGemmThreads), smem, st, g);
   } else if (gemv) {
     const dim3 ggrid((d.d_c + d.d_rope) / kGvCols);
-    const bool fp8 = d.cache_dtype == MLA_FP8_E4M3;
+    const bool fp8 = coded;
     if (n_tokens == 1)
       launch_err = fp8 ? launch_pdl(append_gemv_kernel<MLA_FP8_E4M3, 1>, ggrid, dim3(kGvThreads), 0, st, a)
                        : launch_pdl(append_gemv_kernel<MLA_BF16, 1>, ggrid, dim3(kGvThreads), 0, st, a);
@@ -945,11 +983,15 @@ cudaError_t launch_append(const mla_dims& d, const void* h, int n_tokens, const 
   trace_record(MLA_TRACE_APPEND_PROJECT, true, st);
   if (e != cudaSuccess) return e;
   trace_record(MLA_TRACE_APPEND_FINALIZE, false, st);
-  if (d.cache_dtype != MLA_FP8_E4M3) {
+  if (!coded) {
     trace_record(MLA_TRACE_APPEND_FINALIZE, true, st);
     return e;
   }
-  e = launch_pdl(append_fp8_finalize_kernel, dim3(n_tokens), dim3(128), 0, st, a);
+  if (d.cache_dtype == MLA_FP4_E2M1)
+    e = launch_append_fp4_finalize(d, raw, n_tokens, seq_idx, pos, page_table, batch, max_pages, pool, num_pages,
+                                   page_bytes, status, st);
+  else
+    e = launch_pdl(append_fp8_finalize_kernel, dim3(n_tokens), dim3(128), 0, st, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   trace_record(MLA_TRACE_APPEND_FINALIZE, true, st);
   return e;

@@ -35,6 +35,23 @@ __device__ __forceinline__ void load_rows(const DecodeParams& p, int page, int r
         v = __bfloat162float(kr[(size_t)row * d_r + (j - d_c)]);
       dst[r * DP + j] = v;
     }
+  } else if (CACHE == MLA_FP4_E2M1) {
+    const Fp4Page f4 = fp4_page(p.d.page_size, d_c, d_r);
+    const float* ts = reinterpret_cast<const float*>(pg + f4.ts_off);
+    const __nv_bfloat16* kr = reinterpret_cast<const __nv_bfloat16*>(pg + f4.kr_off);
+    const int W = d_c / 2 + d_r;  // a code byte gives two values
+    for (int i = threadIdx.x; i < nrows * W; i += blockDim.x) {
+      const int r = i / W, j = i % W, row = row0 + r;
+      if (j < d_c / 2) {
+        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)pg[(size_t)row * (d_c / 2) + j], __NV_E2M1);
+        const float2 v = __half22float2(__half2(h));
+        const float s = e4m3_to_float(pg[f4.sc_off + (size_t)row * (d_c / 16) + j / 8]) * ts[row];
+        dst[r * DP + 2 * j] = v.x * s;
+        dst[r * DP + 2 * j + 1] = v.y * s;
+      } else {
+        dst[r * DP + d_c + (j - d_c / 2)] = __bfloat162float(kr[(size_t)row * d_r + (j - d_c / 2)]);
+      }
+    }
   } else {
     using CT = typename std::conditional<CACHE == MLA_F32, float, __nv_bfloat16>::type;
     const CT* src = reinterpret_cast<const CT*>(pg) + (size_t)row0 * D;
@@ -183,6 +200,9 @@ cudaError_t launch_decode_simt(const DecodeParams& p, cudaStream_t st) {
       return launch_simt_typed<MLA_F32, float>(p, st);
     case MLA_BF16:
       return f32 ? launch_simt_typed<MLA_BF16, float>(p, st) : launch_simt_typed<MLA_BF16, __nv_bfloat16>(p, st);
+    case MLA_FP4_E2M1:
+      return f32 ? launch_simt_typed<MLA_FP4_E2M1, float>(p, st)
+                 : launch_simt_typed<MLA_FP4_E2M1, __nv_bfloat16>(p, st);
     default:
       return f32 ? launch_simt_typed<MLA_FP8_E4M3, float>(p, st)
                  : launch_simt_typed<MLA_FP8_E4M3, __nv_bfloat16>(p, st);

@@ -63,7 +63,7 @@ int check_dims(const mla_dims* d) {
   if (!(d->softmax_scale > 0.f) || !isfinite(d->softmax_scale) || !(d->rope_base > 0.f) || !isfinite(d->rope_base))
     return MLA_ERR_INVALID_ARG;
   if (d->act_dtype != MLA_F32 && d->act_dtype != MLA_BF16) return MLA_ERR_INVALID_ARG;
-  if (d->cache_dtype != MLA_F32 && d->cache_dtype != MLA_BF16 && d->cache_dtype != MLA_FP8_E4M3)
+  if (d->cache_dtype != MLA_F32 && d->cache_dtype != MLA_BF16 && !is_coded_cache(*d))
     return MLA_ERR_INVALID_ARG;
   if (d->cache_dtype == MLA_F32 && d->act_dtype != MLA_F32) return MLA_ERR_UNSUPPORTED;
   if (d->cache_dtype == MLA_FP8_E4M3 && d->d_c % 128) return MLA_ERR_UNSUPPORTED;
@@ -78,7 +78,8 @@ int auto_splits(const mla_dims& d, int batch, int n_q) {
   const int sms = num_sms();
   if (!(d.flags & MLA_FLAG_FORCE_SIMT) && decode_tc_supported(d, n_q)) return decode_tc_auto_splits(sms, n_q);
   const int hg = d.n_heads % 8 == 0 && d.d_c / 16 <= 32 ? 8 : 4;
-  const int per_split = n_q * (d.n_heads / hg);
+  const int groups = d.n_heads / hg;  // 0 where no SIMT kernel takes these heads either
+  const int per_split = n_q * (groups > 0 ? groups : 1);
   int w = (4 * sms + per_split - 1) / per_split;
   return w < 1 ? 1 : (w > combine_max_splits() ? combine_max_splits() : w);
 }

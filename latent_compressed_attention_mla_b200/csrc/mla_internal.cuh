@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -39,6 +40,29 @@ __host__ __device__ inline Fp8Page fp8_page(int page_size, int d_c, int d_rope) 
   p.kr_off = a128((size_t)page_size * d_c);
   p.sc_off = a128(p.kr_off + (size_t)page_size * d_rope * 2);
   return p;
+}
+
+// ----------------------------------------------------------------------------
+// 4-bit cache page: [page_size][d_c/2] bytes of e2m1 code pairs (element 2i in
+// the low half of byte i), [page_size][d_rope] bf16 k^R, [page_size][d_c/16]
+// e4m3 block scales, [page_size] fp32 token scales (powers of two), each
+// sub-block 128-byte aligned.  c = code * block scale * token scale.
+// ----------------------------------------------------------------------------
+struct Fp4Page {
+  size_t kr_off, sc_off, ts_off, bytes;
+};
+__host__ __device__ inline Fp4Page fp4_page(int page_size, int d_c, int d_rope) {
+  Fp4Page p;
+  p.kr_off = a128((size_t)page_size * (d_c / 2));
+  p.sc_off = a128(p.kr_off + (size_t)page_size * d_rope * 2);
+  p.ts_off = a128(p.sc_off + (size_t)page_size * (d_c / 16));
+  p.bytes = a128(p.ts_off + (size_t)page_size * 4);
+  return p;
+}
+// Offset of the bf16 k^R rows in a page of a quantised cache.
+__host__ __device__ inline size_t coded_kr_off(int cache_dtype, int page_size, int d_c, int d_rope) {
+  return cache_dtype == MLA_FP4_E2M1 ? fp4_page(page_size, d_c, d_rope).kr_off
+                                     : fp8_page(page_size, d_c, d_rope).kr_off;
 }
 
 // ----------------------------------------------------------------------------
@@ -112,6 +136,46 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t code) {
   return float(v);
 }
 
+// ----------------------------------------------------------------------------
+// The 4-bit quantiser.  A token's scale ts is a power of two taken from
+// a = max(max|c|, max|k^R| / 64), a block's e4m3 scale s from its own maximum,
+// so that every decision below is one fp32 division rounded to the target
+// type; s * ts is exact in fp32.  Dividing k^R into the token scale keeps
+// k^R / ts inside f16 (at most 2^12) for the attention kernel that scores in
+// units of ts.  Non-finite elements take no part in the maxima; their block's
+// scale is the e4m3 NaN, so the row's values there read as NaN.
+// ----------------------------------------------------------------------------
+constexpr int kFp4MinExp = -100;        // smallest token scale 2^-100
+constexpr uint32_t kE4M3NaN = 0x7Fu;
+__device__ __forceinline__ float fp4_token_scale(float amax_c, float amax_kr) {
+  const float a = fmaxf(amax_c, amax_kr * 0.015625f);
+  // floor(log2 a) from the exponent field (a subnormal lands below the limit)
+  const int k = max((int)(__float_as_uint(a) >> 23) - 127 - 5, kFp4MinExp);
+  return a > 0.f ? __uint_as_float((uint32_t)(k + 127) << 23) : 1.0f;
+}
+__device__ __forceinline__ uint32_t fp4_block_scale(float amax, float ts, bool finite) {
+  if (!finite) return kE4M3NaN;
+  return (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f * ts), __NV_SATFINITE, __NV_E4M3);
+}
+// codes of two elements, the first in the low half; step = block scale * ts
+__device__ __forceinline__ uint32_t fp4_pair(float v0, float v1, float step) {
+  if (!(step > 0.f)) return 0u;
+  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(__fdiv_rn(v0, step), __fdiv_rn(v1, step)), __NV_E2M1,
+                                            cudaRoundNearest);
+}
+// |v| for the maxima: non-finite elements count as 0 and clear `finite`
+__device__ __forceinline__ float finite_abs(float v, bool& finite) {
+  const float x = fabsf(v);
+  const bool f = x < INFINITY;
+  finite = finite && f;
+  return f ? x : 0.f;
+}
+// Eight codes (one 32-bit word, first code in the low bits) as exact f16 pairs.
+__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, __half2 (&h)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w >> (8 * i)) & 0xFFu), __NV_E2M1));
+}
+
 // RoPE frequency of rotation pair i of a d_rope-wide vector: base^(-i/half),
 // in double precision.
 __device__ __forceinline__ double rope_inv_freq(int i, int half, float base) {
@@ -157,6 +221,10 @@ struct DecodeLayout {
   size_t off_plan, off_q, off_o, off_lse, total;
   int splits, n_slots;
 };
+
+inline bool is_coded_cache(const mla_dims& d) {
+  return d.cache_dtype == MLA_FP8_E4M3 || d.cache_dtype == MLA_FP4_E2M1;
+}
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -254,6 +322,12 @@ cudaError_t launch_append(const mla_dims& d, const void* h, int n_tokens, const 
 // fp32 scratch (floats) with which launch_append takes its split-K path for
 // these dims and token count, or 0 when that path does not apply
 size_t append_splitk_floats(const mla_dims& d, int n_tokens);
+
+// 4-bit caches: c rows of fp32 scratch -> codes and scales of the rows whose
+// k^R the projection has already stored
+cudaError_t launch_append_fp4_finalize(const mla_dims& d, const float* raw, int n_tokens, const int32_t* seq_idx,
+                                       const int32_t* pos, const int32_t* page_table, int batch, int max_pages,
+                                       void* pool, int num_pages, size_t page_bytes, int* status, cudaStream_t st);
 
 // absorb + split plan (+ empty-split initialisation of the lse slots)
 cudaError_t launch_absorb_and_plan(const mla_dims& d, const void* q_nope, const void* q_rope, const void* W_uk,

@@ -16,7 +16,7 @@
 // 2 * 512 * 2 * 128 per (key, head) once per step.
 //
 // Per sequence, four kernels:
-//   1. gather: the sequence's latent rows c_s (dequantised for an FP8 cache)
+//   1. gather: the sequence's latent rows c_s (dequantised for an FP8 or 4-bit cache)
 //      and k^R_s, from the paged cache into contiguous bf16 rows, zero up to
 //      the next multiple of 128 keys;
 //   2. up-projection: K^C = C W_uk^T and V = C W_uv^T, a tcgen05 GEMM whose
@@ -53,7 +53,7 @@ struct PrefillArgs {
   const int32_t* page_table;
   int max_pages;
   const int32_t* seq_lens;
-  int n_heads, n_q, max_seq_len, fp8;
+  int n_heads, n_q, max_seq_len, cache_dtype;
   float rope_base, scale_log2;
   int max_rows;       // max_seq_len rounded up to a whole 128-key tile
   __nv_bfloat16* C;   // [max_rows, 512]
@@ -95,13 +95,36 @@ __device__ __forceinline__ void gather_row(const PrefillArgs& a, int b, int S, i
   }
   const int row = s % kPPage;
   const uint8_t* pg = a.pool + (size_t)page * a.page_bytes;
-  if (!a.fp8) {
+  if (a.cache_dtype == MLA_BF16) {
     const uint4* src = reinterpret_cast<const uint4*>(pg + (size_t)row * (kPDc + kPDr) * 2);
     for (int u = lane; u < (kPDc + kPDr) / 8; u += 32) {
       const uint4 v = src[u];
       if (u < kPDc / 8) c_dst[u] = v;
       else kr_dst[u - kPDc / 8] = v;
     }
+    return;
+  }
+  if (a.cache_dtype == MLA_FP4_E2M1) {
+    // 16 codes (one block) per lane; code * block scale * token scale has at
+    // most six significant bits, so the bf16 value is exact
+    const Fp4Page f4 = fp4_page(kPPage, kPDc, kPDr);
+    const uint2 w = reinterpret_cast<const uint2*>(pg + (size_t)row * (kPDc / 2))[lane];
+    const float scale = e4m3_to_float(pg[f4.sc_off + (size_t)row * (kPDc / 16) + lane]) *
+                        reinterpret_cast<const float*>(pg + f4.ts_off)[row];
+    __half2 h[8];
+    e2m1x8_to_half2(w.x, *reinterpret_cast<__half2(*)[4]>(&h[0]));
+    e2m1x8_to_half2(w.y, *reinterpret_cast<__half2(*)[4]>(&h[4]));
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = __half22float2(h[i]);
+      const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * scale, f.y * scale);
+      o[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    c_dst[2 * lane] = make_uint4(o[0], o[1], o[2], o[3]);
+    c_dst[2 * lane + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+    if (lane < kPDr / 8)
+      kr_dst[lane] = reinterpret_cast<const uint4*>(pg + f4.kr_off + (size_t)row * kPDr * 2)[lane];
     return;
   }
   // FP8: 16 codes per lane, times the scale of their 128-column tile, rounded to bf16
@@ -642,7 +665,7 @@ PrefillLayout prefill_layout(const mla_dims& d, int max_seq_len) {
 
 bool prefill_supported(const mla_dims& d) {
   return d.d_c == kPDc && d.d_rope == kPDr && d.d_nope == kPDn && d.d_v == kPDv && d.page_size == kPPage &&
-         d.act_dtype == MLA_BF16 && (d.cache_dtype == MLA_BF16 || d.cache_dtype == MLA_FP8_E4M3);
+         d.act_dtype == MLA_BF16 && (d.cache_dtype == MLA_BF16 || is_coded_cache(d));
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -686,7 +709,7 @@ extern "C" int mla_prefill(const mla_dims* dims, const void* q_nope, const void*
   a.n_heads = dims->n_heads;
   a.n_q = n_q;
   a.max_seq_len = max_seq_len;
-  a.fp8 = dims->cache_dtype == MLA_FP8_E4M3;
+  a.cache_dtype = dims->cache_dtype;
   a.rope_base = dims->rope_base;
   a.scale_log2 = dims->softmax_scale * kLog2e;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

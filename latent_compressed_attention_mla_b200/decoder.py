@@ -37,6 +37,11 @@ class MlaDecodeSession:
     def append(self, h, seq_idx, pos, W_dkv, W_kr, page_table, cache_pool, stream=None):
         B.mla_append_latent(self.dims, h, seq_idx, pos, W_dkv, W_kr, page_table, cache_pool, self.append_ws, stream)
 
+    def append_rows(self, c, k_rope, seq_idx, pos, page_table, cache_pool, norm_weight=None, norm_eps=1e-6,
+                    stream=None):
+        """Append rows that the caller has projected (mla_append_rows)."""
+        B.mla_append_rows(self.dims, c, k_rope, seq_idx, pos, page_table, cache_pool, norm_weight, norm_eps, stream)
+
     def attend(self, q_nope, q_rope, W_uk, W_uv, cache_pool, page_table, seq_lens, out=None, lse=None, stream=None):
         out = self.out if out is None else out
         lse = self.lse if lse is None else lse
@@ -65,6 +70,15 @@ class MlaDecodeSession:
         """Append the step's tokens, then attend (the page's order: the new token
         is in the cache before it attends)."""
         self.append(h, seq_idx, pos, weights["W_dkv"], weights["W_kr"], page_table, cache_pool, stream)
+        return self.attend(q_nope, q_rope, weights["W_uk"], weights["W_uv"], cache_pool, page_table, seq_lens,
+                           out, lse, stream)
+
+    def step_rows(self, c, k_rope, seq_idx, pos, q_nope, q_rope, seq_lens, weights: dict, page_table, cache_pool,
+                  out=None, lse=None, stream=None):
+        """`step` for a caller with its own down-projection: append the projected
+        rows (normalised with weights["norm"] where that is given), then attend."""
+        self.append_rows(c, k_rope, seq_idx, pos, page_table, cache_pool, weights.get("norm"),
+                         weights.get("norm_eps", 1e-6), stream)
         return self.attend(q_nope, q_rope, weights["W_uk"], weights["W_uv"], cache_pool, page_table, seq_lens,
                            out, lse, stream)
 

@@ -3,9 +3,11 @@
 Layouts (include/mla.h): an f32/bf16 page is [page_size][d_c + d_rope] rows
 [c | k^R]; an FP8 page is [page_size][d_c] e4m3 codes, then [page_size][d_rope]
 bf16 k^R, then [page_size][d_c/128] fp32 scales, each sub-block starting on a
-128-byte boundary.  Token `pos` of sequence b sits in row pos % page_size of
+128-byte boundary; a 4-bit page is [page_size][d_c/2] e2m1 code pairs, then
+[page_size][d_rope] bf16 k^R, then [page_size][d_c/16] e4m3 block scales, then
+[page_size] fp32 token scales, likewise aligned.  Token `pos` of sequence b sits in row pos % page_size of
 page page_table[b, pos // page_size].  This module only places and reads rows;
-it does no arithmetic on them.
+it does no arithmetic on them (`append` and `values` call the library).
 """
 from __future__ import annotations
 
@@ -41,6 +43,11 @@ class PagedLatentCache:
             return P * (dc + dr) * 4
         if dims.cache_dtype == B.MLA_BF16:
             return P * (dc + dr) * 2
+        if dims.cache_dtype == B.MLA_FP4_E2M1:
+            kr_off = _a128(P * (dc // 2))
+            sc_off = _a128(kr_off + P * dr * 2)
+            ts_off = _a128(sc_off + P * (dc // 16))
+            return _a128(ts_off + P * 4)
         kr_off = _a128(P * dc)
         sc_off = _a128(kr_off + P * dr * 2)
         return _a128(sc_off + P * (dc // 128) * 4)
@@ -59,6 +66,14 @@ class PagedLatentCache:
             return {"codes": self._view(torch.uint8, 0, self.d_c),
                     "kr": self._view(torch.bfloat16, kr_off, self.d_r),
                     "scales": self._view(torch.float32, sc_off, self.d_c // 128)}
+        if self.dims.cache_dtype == B.MLA_FP4_E2M1:
+            kr_off = _a128(self.P * (self.d_c // 2))
+            sc_off = _a128(kr_off + self.P * self.d_r * 2)
+            ts_off = _a128(sc_off + self.P * (self.d_c // 16))
+            return {"codes": self._view(torch.uint8, 0, self.d_c // 2),
+                    "kr": self._view(torch.bfloat16, kr_off, self.d_r),
+                    "scales": self._view(torch.uint8, sc_off, self.d_c // 16),
+                    "ts": self._view(torch.float32, ts_off, 1)}
         dt = torch.float32 if self.dims.cache_dtype == B.MLA_F32 else torch.bfloat16
         rows = self._view(dt, 0, self.d_c + self.d_r)
         return {"c": rows[..., :self.d_c], "kr": rows[..., self.d_c:]}
@@ -77,3 +92,15 @@ class PagedLatentCache:
     def read_rows(self, page_table_row, positions) -> dict:
         pages, r = self.slots(page_table_row, positions)
         return {k: x[pages, r] for k, x in self.views().items()}
+
+    def append(self, c, k_rope, seq_idx, pos, page_table, norm_weight=None, norm_eps: float = 1e-6, stream=None):
+        """Write projected rows through mla_append_rows (norm, rotation, rounding to the cache type)."""
+        B.mla_append_rows(self.dims, c, k_rope, seq_idx, pos, page_table, self.pool, norm_weight, norm_eps, stream)
+
+    def values(self, seq_idx, pos, page_table, stream=None):
+        """(c [N, d_c], k^R [N, d_rope]) of cache rows in the activation type, through mla_read_rows."""
+        n, act = seq_idx.numel(), B.act_dtype(self.dims)
+        c = torch.empty(n, self.d_c, dtype=act, device=self.pool.device)
+        kr = torch.empty(n, self.d_r, dtype=act, device=self.pool.device)
+        B.mla_read_rows(self.dims, self.pool, page_table, seq_idx, pos, c, kr, stream)
+        return c, kr

@@ -120,7 +120,7 @@ class MlaConfig:
     T: int
     L: tuple  # per-sequence cached length before the step
     act_dtype: str  # "f32" | "bf16"
-    cache_dtype: str  # "f32" | "bf16" | "fp8"
+    cache_dtype: str  # "f32" | "bf16" | "fp8" | "fp4"
     page_size: int = 64
     rope_base: float = 10000.0
     spare_pages: int = 0
@@ -257,7 +257,10 @@ def history_rows(cfg: MlaConfig, b: int, s0: int, s1: int, device="cpu") -> dict
 
     f32/bf16 caches: {"c": [n, d_c], "kr": [n, d_rope]} in the cache dtype.
     fp8 cache: {"codes": uint8 [n, d_c], "scales": f32 [n, d_c/128],
-    "kr": bf16 [n, d_rope]} where the latent value is e4m3(codes) * scale."""
+    "kr": bf16 [n, d_rope]} where the latent value is e4m3(codes) * scale.
+    fp4 cache: {"codes": uint8 [n, d_c/2] uniform code pairs, "scales": uint8
+    [n, d_c/16] e4m3 codes of 4, 4.5 .. 7.5, "ts": f32 [n, 1] = 2^-4, "kr"}
+    (values of variance near one)."""
     n = s1 - s0
     r0 = int(history_row_offsets(cfg)[b]) + s0
     dc, dr = cfg.d_c, cfg.d_rope
@@ -269,6 +272,12 @@ def history_rows(cfg: MlaConfig, b: int, s0: int, s1: int, device="cpu") -> dict
         scales = ((u * 0.25 + 0.875) * float(np.float32(1.0 / FP8_CODE_GAIN))).view(n, nt)
         kr = normal(cfg.seed, S_HIST_KR, n * dr, device, start=r0 * dr).view(n, dr).to(torch.bfloat16)
         return {"codes": codes, "scales": scales, "kr": kr}
+    if cfg.cache_dtype == "fp4":
+        codes = (uniform(cfg.seed, S_HIST_C, n * dc // 2, device, start=r0 * dc // 2) * 256).to(torch.uint8)
+        scales = (uniform(cfg.seed, S_HIST_SCALE, n * dc // 16, device, start=r0 * dc // 16) * 8).to(torch.uint8) + 0x48
+        kr = normal(cfg.seed, S_HIST_KR, n * dr, device, start=r0 * dr).view(n, dr).to(torch.bfloat16)
+        return {"codes": codes.view(n, dc // 2), "scales": scales.view(n, dc // 16),
+                "ts": torch.full((n, 1), 0.0625, device=device), "kr": kr}
     dt = torch.float32 if cfg.cache_dtype == "f32" else torch.bfloat16
     c = normal(cfg.seed, S_HIST_C, n * dc, device, start=r0 * dc).view(n, dc).to(dt)
     kr = normal(cfg.seed, S_HIST_KR, n * dr, device, start=r0 * dr).view(n, dr).to(dt)

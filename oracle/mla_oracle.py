@@ -124,6 +124,64 @@ def fp8_dequantise_latent(codes, scales) -> np.ndarray:
     return (v * np.asarray(scales, dtype=np.float64)[..., None]).reshape(n, dc)
 
 
+# 4-bit rows: OCP E2M1 codes (S.EE.M, bias 1) in blocks of 16 with an e4m3 scale
+# each and a power-of-two scale per token.
+E2M1_POS = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def e2m1_encode(x) -> np.ndarray:
+    """Nearest e2m1 code (ties to the even code), saturating at +-6."""
+    x = np.asarray(x, dtype=np.float64)
+    d = np.abs(np.abs(x)[..., None] - E2M1_POS)
+    best = d.min(axis=-1, keepdims=True)
+    # of two equally near codes (neighbours) the even one
+    score = np.where(d == best, np.arange(8) % 2, 2)
+    mag = np.argmin(score, axis=-1)
+    return (mag | np.where(np.signbit(x) & (mag > 0), 8, 0)).astype(np.uint8)
+
+
+def e2m1_decode(codes) -> np.ndarray:
+    codes = np.asarray(codes, dtype=np.uint8)
+    return np.where(codes & 8, -1.0, 1.0) * E2M1_POS[codes & 7]
+
+
+def fp4_quantise_latent(c, kr) -> tuple[np.ndarray, np.ndarray, np.ndarray]:
+    """Rows c [n, d_c] and their stored k^R [n, d_R] -> (code pairs uint8
+    [n, d_c/2], e4m3 scale codes uint8 [n, d_c/16], token scales [n, 1]).  The
+    decisions are taken in fp32, from the fp32 value of c."""
+    c32 = np.asarray(c, dtype=np.float64).astype(np.float32)
+    kr = np.asarray(kr, dtype=np.float64)
+    n, dc = c32.shape
+    ok = np.isfinite(c32)
+    mag = np.where(ok, np.abs(c32), np.float32(0)).astype(np.float64)
+    kmag = np.where(np.isfinite(kr), np.abs(kr), 0.0)
+    a = np.maximum(mag.max(axis=1), kmag.max(axis=1, initial=0.0) / 64)
+    _, e = np.frexp(a)  # a in [2^(e-1), 2^e)
+    ts = np.where(a > 0, np.ldexp(1.0, np.maximum(e - 6, -100)), 1.0)[:, None]
+    blocks = np.where(ok, c32, np.float32(0)).astype(np.float64).reshape(n, dc // 16, 16)
+    bad = ~ok.reshape(n, dc // 16, 16).all(axis=-1)
+    amax = np.abs(blocks).max(axis=-1)
+    s = e4m3_encode(to_f32(amax / (6.0 * ts)))
+    step = (e4m3_decode(s) * ts)[..., None]
+    q = to_f32(np.divide(blocks, step, out=np.zeros_like(blocks), where=step > 0))
+    codes = np.where(bad[..., None], 0, e2m1_encode(q)).astype(np.uint8).reshape(n, dc)
+    s = np.where(bad, 0x7F, s).astype(np.uint8)
+    return codes[:, 0::2] | (codes[:, 1::2] << 4), s, ts
+
+
+def fp4_dequantise_latent(codes, scales, ts) -> np.ndarray:
+    codes = np.asarray(codes, dtype=np.uint8)
+    n, dc = codes.shape[0], 2 * codes.shape[1]
+    v = np.stack([e2m1_decode(codes & 15), e2m1_decode(codes >> 4)], axis=-1).reshape(n, dc // 16, 16)
+    return (v * e4m3_decode(scales)[..., None]).reshape(n, dc) * np.asarray(ts, dtype=np.float64).reshape(n, 1)
+
+
+def rms_norm(c, weight, eps: float) -> np.ndarray:
+    """weight * c / sqrt(mean(c^2) + eps) over the last axis."""
+    c = np.asarray(c, dtype=np.float64)
+    return np.asarray(weight, dtype=np.float64) * c / np.sqrt((c * c).mean(axis=-1, keepdims=True) + eps)
+
+
 # ----------------------------------------------------------------------------
 # Decoupled RoPE  ([N1] decoding module, apply_rope; [MW] A.)
 # ----------------------------------------------------------------------------
@@ -164,7 +222,8 @@ def append_latent(h, W_dkv, W_kr, pos, base: float = 10000.0):
 
 def encode_cache_rows(c, kr, cache_dtype: str) -> dict:
     """Round appended rows to the cache's storage format.  f32/bf16: {"c", "kr"}
-    as float64 values of that format; fp8: {"codes", "scales", "kr"}."""
+    as float64 values of that format; fp8: {"codes", "scales", "kr"}; fp4: those
+    and the token scales "ts"."""
     if cache_dtype == "f32":
         return {"c": to_f32(c), "kr": to_f32(kr)}
     if cache_dtype == "bf16":
@@ -172,11 +231,17 @@ def encode_cache_rows(c, kr, cache_dtype: str) -> dict:
     if cache_dtype == "fp8":
         codes, scales = fp8_quantise_latent(c)
         return {"codes": codes, "scales": scales, "kr": to_bf16(kr)}
+    if cache_dtype == "fp4":
+        kr = to_bf16(kr)
+        codes, scales, ts = fp4_quantise_latent(c, kr)
+        return {"codes": codes, "scales": scales, "ts": ts, "kr": kr}
     raise ValueError(cache_dtype)
 
 
 def decode_cache_rows(rows: dict) -> tuple[np.ndarray, np.ndarray]:
     """Cache rows -> (c, k^R) float64 values the attention sees."""
+    if "ts" in rows:
+        return fp4_dequantise_latent(rows["codes"], rows["scales"], rows["ts"]), np.asarray(rows["kr"], np.float64)
     if "codes" in rows:
         return fp8_dequantise_latent(rows["codes"], rows["scales"]), np.asarray(rows["kr"], np.float64)
     return np.asarray(rows["c"], np.float64), np.asarray(rows["kr"], np.float64)
@@ -322,6 +387,8 @@ def cache_bytes_per_token(d_c: int, d_rope: int, cache_dtype: str) -> int:
         return 2 * (d_c + d_rope)
     if cache_dtype == "fp8":
         return d_c + 2 * d_rope + 4 * (d_c // 128)
+    if cache_dtype == "fp4":
+        return d_c // 2 + 2 * d_rope + d_c // 16 + 4
     raise ValueError(cache_dtype)
 
 

@@ -1,0 +1,137 @@
+"""Attention over a 4-bit latent cache against the oracle (float64): every
+decode path, prefill, and whole steps (append, then attend).
+
+The stored values are exact on both sides, so the differences are the
+attention's own: the bars of the other caches apply (max|gpu - oracle| /
+max|oracle| of 1e-5 with fp32 activations, 1e-2 with bf16)."""
+import numpy as np
+import pytest
+import torch
+
+from latent_compressed_attention_mla_b200 import binding as B
+from latent_compressed_attention_mla_b200 import workloads as W
+from oracle import mla_oracle as O
+from tests.gpu_harness import GpuProblem, OracleProblem, rel_err, tolerance
+
+pytestmark = pytest.mark.gpu
+
+
+class Fp4Oracle(OracleProblem):
+    def history(self, b):
+        rows = W.history_rows(self.cfg, b, 0, int(self.cfg.L[b]), "cpu")
+        return O.decode_cache_rows({k: v.double().numpy() if k in ("ts", "kr") else v.numpy() for k, v in rows.items()})
+
+    def after(self, gp, b):
+        """Cache values of sequence b with the step's rows read back from the device cache
+        (the append's own rounding is tested apart)."""
+        C0, KR0 = self.history(b)
+        n = np.nonzero(self.seq_idx == b)[0]
+        idx = torch.from_numpy(n)
+        c, kr = gp.cache.values(gp.seq_idx[idx.cuda()].contiguous(), gp.pos[idx.cuda()].contiguous(), gp.page_table)
+        return np.concatenate([C0, c.double().cpu().numpy()]), np.concatenate([KR0, kr.double().cpu().numpy()])
+
+
+def fp4_cfg(name="fp4", **kw):
+    base = W.V3_FP8_B128_T2.with_(cache_dtype="fp4", name=name)
+    return base.with_(**kw)
+
+
+def check(cfg, flags=0, num_splits=0, step=True, path=None):
+    gp = GpuProblem(cfg, flags=flags, num_splits=num_splits)
+    if path is not None:
+        assert B.decode_path(gp.dims, cfg.T) == path
+    gp.session.append(gp.inputs["h"], gp.seq_idx, gp.pos, gp.weights["W_dkv"], gp.weights["W_kr"], gp.page_table,
+                      gp.cache.pool)
+    out, lse = gp.attend_only()
+    assert gp.status() == 0
+    op = Fp4Oracle(cfg)
+    for b in range(cfg.B):
+        o, l, _ = O.decode_absorbed(op.inp["q_nope"][b], op.inp["q_rope"][b], *op.after(gp, b), op.w["W_uk"],
+                                    op.w["W_uv"], int(cfg.seq_lens[b]), cfg.softmax_scale, cfg.rope_base)
+        assert rel_err(out[b].double().cpu().numpy(), o) <= tolerance(cfg), b
+        assert np.abs(lse[b].double().cpu().numpy() - l).max() <= tolerance(cfg) * max(1.0, np.abs(l).max()), b
+    return gp, op
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_simt_fp32_activations(T):
+    cfg = W.TINY_F32.with_(cache_dtype="fp4", T=T, B=2, L=(5, 200), name=f"tiny-fp4-{T}")
+    check(cfg)
+
+
+@pytest.mark.parametrize("page,d_c,d_rope", [(32, 64, 16), (96, 128, 2), (64, 512, 64), (64, 160, 6)])
+def test_simt_other_dims(page, d_c, d_rope):
+    cfg = W.TINY_F32.with_(cache_dtype="fp4", B=2, L=(1, 90), page_size=page, d_c=d_c, d_rope=d_rope,
+                           name=f"tiny-fp4-{d_c}-{d_rope}-{page}")
+    check(cfg)
+
+
+@pytest.mark.parametrize("heads", [4, 16, 128])
+def test_simt_bf16_activations(heads):
+    cfg = fp4_cfg(n_heads=heads, B=2, T=2, L=(3, 150))
+    check(cfg, flags=B.MLA_FLAG_FORCE_SIMT, path=0)
+
+
+@pytest.mark.parametrize("L,T,heads", [(0, 1, 2), (0, 200, 2), (100, 129, 3), (300, 64, 1)])
+def test_prefill(L, T, heads):
+    cfg = fp4_cfg(n_heads=heads, B=2, T=T, L=(L, L + 7))
+    gp = GpuProblem(cfg)
+    i = gp.inputs
+    gp.session.append(i["h"], gp.seq_idx, gp.pos, gp.weights["W_dkv"], gp.weights["W_kr"], gp.page_table, gp.cache.pool)
+    out, lse = gp.session.prefill(i["q_nope"], i["q_rope"], gp.weights["W_uk"], gp.weights["W_uv"], gp.cache.pool,
+                                  gp.page_table, gp.seq_lens, int(cfg.seq_lens.max()))
+    torch.cuda.synchronize()
+    assert gp.status() == 0
+    op = Fp4Oracle(cfg)
+    for b in range(cfg.B):
+        C, KR = op.after(gp, b)
+        o, l = O.decode_explicit(op.inp["q_nope"][b], op.inp["q_rope"][b], C, KR, op.w["W_uk"], op.w["W_uv"],
+                                 int(cfg.seq_lens[b]), cfg.softmax_scale, cfg.rope_base)
+        assert rel_err(out[b].double().cpu().numpy(), o) <= 1e-2
+        assert np.abs(lse[b].double().cpu().numpy() - l).max() <= 1e-2 * max(1.0, np.abs(l).max())
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_step_rows_append_attend_and_read_together(heads):
+    """A caller's own projection: rows with a norm into the 4-bit cache, attention
+    over them, the rows read back; the same step captured and replayed."""
+    cfg = fp4_cfg(n_heads=heads, B=3, T=2, L=(0, 62, 500))
+    gp = GpuProblem(cfg)
+    n = cfg.B * cfg.T
+    kv = (W.normal(9, 1, n * 576).view(n, 576) * 2).to(torch.bfloat16).cuda()
+    weights = dict(gp.weights, norm=(W.uniform(9, 2, 512) + 0.5).to(torch.bfloat16).cuda(), norm_eps=1e-5)
+    i = gp.inputs
+
+    def step():
+        return gp.session.step_rows(kv[:, :512], kv[:, 512:], gp.seq_idx, gp.pos, i["q_nope"], i["q_rope"],
+                                    gp.seq_lens, weights, gp.page_table, gp.cache.pool)
+
+    out, _ = step()
+    torch.cuda.synchronize()
+    first = out.clone()
+    op = Fp4Oracle(cfg)
+    c = O.rms_norm(kv[:, :512].double().cpu().numpy(), weights["norm"].double().cpu().numpy(), 1e-5)
+    kr = O.apply_rope(kv[:, 512:].double().cpu().numpy(), op.pos)
+    enc = O.encode_cache_rows(c, kr, "fp4")
+    C1, KR1 = O.decode_cache_rows(enc)
+    gc, gk = gp.cache.values(gp.seq_idx, gp.pos, gp.page_table)
+    assert np.array_equal(gc.double().cpu().numpy(), C1)
+    assert np.abs(gk.double().cpu().numpy() - KR1).max() <= 2.0 ** -7 * np.abs(KR1).max()
+    for b in range(cfg.B):
+        s = op.seq_idx == b
+        C0, KR0 = op.history(b)
+        o, _, _ = O.decode_absorbed(op.inp["q_nope"][b], op.inp["q_rope"][b], np.concatenate([C0, C1[s]]),
+                                    np.concatenate([KR0, KR1[s]]), op.w["W_uk"], op.w["W_uv"], int(cfg.seq_lens[b]),
+                                    cfg.softmax_scale, cfg.rope_base)
+        assert rel_err(first[b].double().cpu().numpy(), o) <= 1e-2
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            step()
+        gp.session.out.zero_()
+        g.replay()
+    side.synchronize()
+    assert torch.equal(gp.session.out, first)
+    assert gp.status() == 0
