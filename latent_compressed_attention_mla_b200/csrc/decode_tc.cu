@@ -1,7 +1,8 @@
 // S3 on the 5th-generation tensor cores: split-KV attention of the absorbed
 // queries over the paged latent cache, DeepSeek-V3 dims (128 heads, 576-wide
-// rows = 512 latent + 64 RoPE, 64-token pages), for a bf16 cache and for an
-// FP8 (e4m3 + per-128-column fp32 scales, bf16 k^R) cache.
+// rows = 512 latent + 64 RoPE, 64-token pages), for a bf16 cache, for an
+// FP8 (e4m3 + per-128-column fp32 scales, bf16 k^R) cache and for a 4-bit
+// (e2m1 + per-16-column e4m3 scales and a token scale, bf16 k^R) cache.
 //
 // What it computes ("DeepSeek MLA Architecture: How Multi-Head Latent Attention
 // Cuts KV Cache by 93%", "3. Decoupled RoPE and Matrix Absorption" and the
@@ -41,6 +42,10 @@
 //    and one cvt + one multiply per element pair), and zero the rows past a
 //    sequence's end.  Queries and probabilities are f16 on this path, so both
 //    MMA operands share the type (kind::f16).
+//  * 4-bit cache: the FP8 scheme with other converters: e2m1 pairs become f16
+//    by one conversion and one multiply with the block's scale times the token's
+//    (at most six significant bits, so exact wherever f16 holds the value's
+//    range).  A staging slot holds 128 columns, enough for two units.
 //  * Warp roles: 0-3 softmax + epilogue (one TMEM lane each), 4 TMEM
 //    allocation and (leader) QK issue, 5 (leader) PV issue; bf16 cache: 6-7
 //    TMA for Q and QK data, 8-9 TMA for PV data; FP8 cache: 6 / 7 TMA for
@@ -73,17 +78,22 @@ constexpr int kQKUnits = kChunks;                     // QK units per tile
 
 constexpr uint32_t kUnitBytes = 16384;                // operand unit: this CTA's share of four MMAs
 constexpr uint32_t kStageBytes = 8192;                // FP8 staging slot: raw page data of one unit
-constexpr uint32_t kSclBytes = kTilePages * 64 * 4 * 4;  // FP8: [4 pages][64 rows][4] fp32 scales of a tile
+// scales of one page: FP8 [64 rows][4] fp32; 4-bit [64 rows][32] e4m3, then [64 rows] fp32 token scales
+template <int kCache>
+constexpr uint32_t kPageScl = kCache == MLA_FP4_E2M1 ? 64 * 32 + 64 * 4 : 64 * 4 * 4;
 constexpr uint32_t kQBytes = kChunks * 64 * 128;      // 73728: 64 heads x 576 (16-bit)
 constexpr uint32_t kPBytes = kTilePages * 64 * 128;   // 32768: 64 heads x 256 keys (16-bit), 4 sub-tiles
 
 // Shared memory layout and warp roles of the two variants (offsets from a
 // 1024-byte aligned base).
-template <bool kFp8>
+template <int kCache>
 struct TcLayout {
-  static constexpr int QKSlots = kFp8 ? 2 : 3, PVSlots = kFp8 ? 2 : 4;
-  static constexpr int QStSlots = kFp8 ? 3 : 0, PStSlots = kFp8 ? 3 : 0;
-  static constexpr int SclBufs = kFp8 ? 2 : 0;  // per-tile scales of the four pages (4 KB each)
+  static constexpr bool kConv = kCache != MLA_BF16;       // converter warps write the operand units
+  static constexpr bool kFp4 = kCache == MLA_FP4_E2M1;
+  static constexpr int QKSlots = kConv ? 2 : 3, PVSlots = kConv ? 2 : 4;
+  static constexpr int QStSlots = kFp4 ? 2 : kConv ? 3 : 0, PStSlots = QStSlots;
+  static constexpr int SclBufs = kConv ? 2 : 0;  // per-tile scales of the four pages
+  static constexpr uint32_t PageScl = kPageScl<kCache>, SclBytes = kTilePages * PageScl;
   static constexpr uint32_t OffQ = 0;
   static constexpr uint32_t OffP = OffQ + kQBytes;
   static constexpr uint32_t OffQKRing = OffP + kPBytes;
@@ -91,7 +101,7 @@ struct TcLayout {
   static constexpr uint32_t OffQSt = OffPVRing + PVSlots * kUnitBytes;
   static constexpr uint32_t OffPSt = OffQSt + QStSlots * kStageBytes;
   static constexpr uint32_t OffScl = OffPSt + PStSlots * kStageBytes;
-  static constexpr uint32_t OffBar = OffScl + SclBufs * kSclBytes;
+  static constexpr uint32_t OffBar = OffScl + SclBufs * SclBytes;
   // barrier indices
   static constexpr int QK_FULL = 0;                     // [QKSlots] leader: unit written in both CTAs
   static constexpr int QK_EMPTY = QK_FULL + QKSlots;    // [QKSlots] each CTA: unit consumed (MMA commit)
@@ -119,16 +129,17 @@ struct TcLayout {
   // warp roles: the FP8 cache moves half the bytes through its producers, so
   // one producer per ring keeps up and leaves registers for the converters
   static constexpr int QKWarp = 4, PVWarp = 5;          // TMEM alloc (QKWarp); leader lane 0 issues the MMAs
-  static constexpr int Producers = kFp8 ? 1 : 2, ConvWarps = 4;
+  static constexpr int Producers = kConv ? 1 : 2, ConvWarps = 4;
   static constexpr int QKProdWarp = 6, PVProdWarp = QKProdWarp + Producers;
   static constexpr int QKConvWarp = PVProdWarp + Producers, PVConvWarp = QKConvWarp + ConvWarps;
-  static constexpr int Threads = 32 * (kFp8 ? PVConvWarp + ConvWarps : PVProdWarp + Producers);
+  static constexpr int Threads = 32 * (kConv ? PVConvWarp + ConvWarps : PVProdWarp + Producers);
   // arrivals completing one phase of a unit's FULL barrier: the leader's
   // expect-tx arrival (bf16), or every converter warp of both CTAs (FP8)
-  static constexpr int UnitFullCount = kFp8 ? 2 * ConvWarps : 1;
+  static constexpr int UnitFullCount = kConv ? 2 * ConvWarps : 1;
 };
-static_assert(TcLayout<false>::SmemBytes <= 232448, "shared memory");
-static_assert(TcLayout<true>::SmemBytes <= 232448, "shared memory");
+static_assert(TcLayout<MLA_BF16>::SmemBytes <= 232448, "shared memory");
+static_assert(TcLayout<MLA_FP8_E4M3>::SmemBytes <= 232448, "shared memory");
+static_assert(TcLayout<MLA_FP4_E2M1>::SmemBytes <= 232448, "shared memory");
 
 // TMEM columns (per CTA, 2x2 layout): S buffers 128 columns each, O 2 x 128
 constexpr uint32_t kTmemCols = 512;
@@ -398,6 +409,27 @@ __device__ __forceinline__ void e4m3x4_scaled(uint32_t w, __half2 s2, uint32_t& 
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// 32 e2m1 codes (16 bytes: two blocks of 16 columns) times their scales -> 64
+// bytes of f16.  s: the blocks' e4m3 scales, the first in the low byte; ts: the
+// token's scale.
+__device__ __forceinline__ void e2m1x32_scaled(const uint4& w, uint32_t s, __half2 ts, uint4 (&o)[4]) {
+  const __half2 sc = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)s, __NV_E4M3)), ts);
+  const __half2 s0 = __low2half2(sc), s1 = __high2half2(sc);
+  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __half2 h[4];
+    e2m1x8_to_half2(words[i], h);
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 v = __hmul2(h[e], i < 2 ? s0 : s1);
+      r[e] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    o[i] = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+}
+
 // Two bf16 (one 32-bit word) -> two f16 (round to nearest).
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
   const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
@@ -449,6 +481,14 @@ struct SegmentWalker {
 // holds pages r and r + 2, so a tile of two pages puts one page in each CTA.
 __device__ __forceinline__ int tile_page(int pos) { return (pos >> 1) + 2 * (pos & 1); }
 
+// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into
+// this CTA's shared memory, completing on a local barrier
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // Bulk prefetch of [ptr, ptr + bytes) into L2 (16-byte aligned, bytes % 16 == 0).
 __device__ __forceinline__ void prefetch_l2(const void* ptr, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
@@ -495,11 +535,12 @@ struct TcParams {
   CUtensorMap map_pv;    // pool rows, box 64 x 64 (one page x 64 columns: QK and PV boxes)
   CUtensorMap map_pv16;  // pool rows, box 64 x 16 (16-key group of a partial page)
   CUtensorMap map_row;   // pool rows, box 64 x 1 (one row of a partial 16-key group)
-  // FP8 cache: [pages][64 rows][...] views of the page sub-blocks
-  CUtensorMap map_codes_qk;  // e4m3 codes, box 64 codes x 64 rows (one page's part of a QK unit)
-  CUtensorMap map_codes_pv;  // e4m3 codes, box 128 codes x 64 rows (one PV unit)
+  // FP8 and 4-bit caches: [pages][64 rows][...] views of the page sub-blocks
+  CUtensorMap map_codes_qk;  // FP8: box 64 codes x 64 rows (one page's part of a QK unit); 4-bit: map_codes_pv's
+  CUtensorMap map_codes_pv;  // box 128 codes (128 or 64 bytes) x 64 rows (one PV unit)
   CUtensorMap map_kr;        // bf16 k^R, box 64 x 64 rows
-  CUtensorMap map_scl;       // fp32 scales, box 4 x 64 rows (one page)
+  CUtensorMap map_scl;       // FP8: fp32 scales, box 4 x 64 rows (one page)
+  size_t scl_off;            // 4-bit: the scales' offset in a page (block scales, then token scales)
 };
 
 // Position in a ring of `slots` slots: slot index and the parity of its use.
@@ -552,14 +593,16 @@ struct RingConsumer {
   }
 };
 
-template <bool kFp8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Threads, 1)
+template <int kCache>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Threads, 1)
     decode_tc_kernel(const __grid_constant__ TcParams P) {
-  using L = TcLayout<kFp8>;
-  using PT = typename std::conditional<kFp8, __half2, __nv_bfloat162>::type;  // P element pair
+  using L = TcLayout<kCache>;
+  constexpr bool kConv = L::kConv, kFp4 = L::kFp4;
+  constexpr int kUnitsPerStage = kFp4 ? 2 : 1;  // operand units that one staging slot of codes feeds
+  using PT = typename std::conditional<kConv, __half2, __nv_bfloat162>::type;  // P element pair
   constexpr int kConvThreads = 32 * L::ConvWarps;  // threads converting one ring's units
-  constexpr uint32_t kIdescQK = idesc(128, 256, false, false, kFp8);
-  constexpr uint32_t kIdescPV = idesc(128, 256, false, true, kFp8);
+  constexpr uint32_t kIdescQK = idesc(128, 256, false, false, kConv);
+  constexpr uint32_t kIdescPV = idesc(128, 256, false, true, kConv);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -650,8 +693,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
     // -------------------------------------------------------------- TMA: Q, QK
     if (lane == 0 && !stall) {
       const int pid = warp - L::QKProdWarp;
-      RingProducer ring{kFp8 ? L::QStSlots : L::QKSlots, L::Producers, pid};
-      const uint32_t empty0 = kFp8 ? bar(L::QST_EMPTY) : bar(L::QK_EMPTY);
+      RingProducer ring{kConv ? L::QStSlots : L::QKSlots, L::Producers, pid};
+      const uint32_t empty0 = kConv ? bar(L::QST_EMPTY) : bar(L::QK_EMPTY);
       const int y_pages = 2 * (int)rank;  // this CTA's key positions of a tile (pages tile_page(...))
       SegmentWalker walk(p, w, t);
       Segment s;
@@ -682,7 +725,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
             const int tp = tile_page(y_pages + i);
             pg[i] = tp < npg ? page_of(s.b, pg0 + tp) : -1;
           }
-          if constexpr (kFp8) {
+          if constexpr (kConv) {
             // this CTA's pages two tiles ahead (at a segment's start also one
             // ahead) go to L2 now, so that the staging loads find them there.
             // (Measured: a gain for the FP8 cache, whose converters bound the
@@ -708,15 +751,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
               ok = mbar_wait(bar(L::SCL_EMPTY + sb), ((gtile >> 1) & 1) ^ 1, abort_flag, p.status);
               if (!ok) break;
               const uint32_t fb = bar(L::SCL_FULL + sb);
-              mbar_arrive_tx_local(fb, kSclBytes);
-              for (int i = 0; i < kTilePages; ++i)
-                tma_load_3d(sbase + L::OffScl + sb * kSclBytes + i * 1024, &P.map_scl, 0, 0,
-                            i < npg ? page_of(s.b, pg0 + i) : -1, fb);
+              mbar_arrive_tx_local(fb, L::SclBytes);
+              for (int i = 0; i < kTilePages; ++i) {
+                const uint32_t dst = sbase + L::OffScl + sb * L::SclBytes + i * L::PageScl;
+                if constexpr (kFp4)  // (a page past the tile's end: the first page's scales, which nothing uses)
+                  bulk_load(dst, p.pool + (size_t)page_of(s.b, pg0 + (i < npg ? i : 0)) * p.page_bytes + P.scl_off,
+                            L::PageScl, fb);
+                else
+                  tma_load_3d(dst, &P.map_scl, 0, 0, i < npg ? page_of(s.b, pg0 + i) : -1, fb);
+              }
             }
             ++gtile;
           }
           for (int c = 0; c < kQKUnits; ++c) {
-            if constexpr (!kFp8) {
+            if constexpr (!kConv) {
               uint32_t slot;
               if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
               if (rank == 0) mbar_expect_tx(bar(L::QK_FULL + slot), 2 * kUnitBytes);
@@ -724,12 +772,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
               for (int i = 0; i < 2; ++i)
                 tma_load_2d_pair(dst + i * 8192, &P.map_pv, 64 * c, pg[i] >= 0 ? pg[i] * kPage : -kPage, fb);
             } else if (c < kChunks - 1) {
-              // codes of columns [64c, 64c+64) of both pages: one staging slot
+              // codes of columns [64c, 64c+64) of both pages (4-bit: of 128
+              // columns, for two units): one staging slot
+              if (c % kUnitsPerStage != 0) continue;
               uint32_t slot;
               if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
               const uint32_t dst = sbase + L::OffQSt + slot * kStageBytes, fb = bar(L::QST_FULL + slot);
               mbar_arrive_tx_local(fb, kStageBytes);
-              for (int i = 0; i < 2; ++i) tma_load_3d(dst + i * 4096, &P.map_codes_qk, 64 * c, 0, pg[i], fb);
+              for (int i = 0; i < 2; ++i)
+                tma_load_3d(dst + i * 4096, &P.map_codes_qk, kFp4 ? 32 * c : 64 * c, 0, pg[i], fb);
             } else {
               // k^R: one staging slot per page
               for (int i = 0; i < 2; ++i) {
@@ -748,8 +799,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
   } else if (warp >= L::PVProdWarp && warp < L::PVProdWarp + L::Producers) {
     // ------------------------------------------------------------------ TMA: PV
     if (lane == 0 && !stall) {
-      RingProducer ring{kFp8 ? L::PStSlots : L::PVSlots, L::Producers, warp - L::PVProdWarp};
-      const uint32_t empty0 = kFp8 ? bar(L::PST_EMPTY) : bar(L::PV_EMPTY);
+      RingProducer ring{kConv ? L::PStSlots : L::PVSlots, L::Producers, warp - L::PVProdWarp};
+      const uint32_t empty0 = kConv ? bar(L::PST_EMPTY) : bar(L::PV_EMPTY);
       const int x_pv = 128 * (int)rank;  // this CTA's 128 columns of an N=256 half
       SegmentWalker walk(p, w, t);
       Segment s;
@@ -766,10 +817,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
             const int valid = tp < npg ? min(kPage, s.nvis - (pg0 + tp) * kPage) : 0;
             const int page = valid > 0 ? page_of(s.b, pg0 + tp) : 0;
             for (int j = 0; j < 2; ++j) {
+              if (kFp4 && j == 1) break;  // one slot holds both halves' codes
               uint32_t slot;
               if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
               const int x0 = 256 * j + x_pv;
-              if constexpr (kFp8) {
+              if constexpr (kFp4) {
+                const uint32_t fb = bar(L::PST_FULL + slot);
+                mbar_arrive_tx_local(fb, kStageBytes);
+                for (int jj = 0; jj < 2; ++jj)
+                  tma_load_3d(sbase + L::OffPSt + slot * kStageBytes + jj * 4096, &P.map_codes_pv, (256 * jj + x_pv) / 2,
+                              0, valid > 0 ? page : -1, fb);
+              } else if constexpr (kConv) {
                 // the converters zero the rows past the visible keys
                 const uint32_t fb = bar(L::PST_FULL + slot);
                 mbar_arrive_tx_local(fb, kStageBytes);
@@ -807,7 +865,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
         }
       }
     }
-  } else if (kFp8 && warp >= L::QKConvWarp && warp < L::QKConvWarp + L::ConvWarps) {
+  } else if (kConv && warp >= L::QKConvWarp && warp < L::QKConvWarp + L::ConvWarps) {
     // ------------------------------------------------- FP8: QK unit conversion
     // Thread ct of the converter warps converts 16-byte groups ct,
     // ct + kConvThreads, ... of the staged data into the unit (128-byte swizzle).
@@ -826,7 +884,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
         ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
         if (!ok) break;
         // the tile's scales, [4 pages][64 rows][4 tiles of 128 columns]
-        const float* scl = reinterpret_cast<const float*>(smem + L::OffScl + (gt & 1) * kSclBytes);
+        const uint8_t* scl_b = smem + L::OffScl + (gt & 1) * L::SclBytes;
+        const float* scl = reinterpret_cast<const float*>(scl_b);
 #ifdef MLA_TC_TRACE
         long long w_unit = 0, w_stage = 0, t_tile = clock64();
 #endif
@@ -842,7 +901,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
 #endif
           if (!ok) break;
           uint8_t* dstu = smem + L::OffQKRing + unit.slot * kUnitBytes;
-          if (c < kChunks - 1) {
+          if (kFp4 && c < kChunks - 1) {
+            // [2 pages][64 rows][128 codes], this unit's 64 of them: group gi is
+            // 32 columns (two blocks) of unit row gi / 2
+            if (c % kUnitsPerStage == 0) {
+              ok = mbar_wait(bar(L::QST_FULL + stage.slot), stage.phase, abort_flag, p.status);
+              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+#ifdef MLA_TC_TRACE
+              w_stage += clock64() - tw;
+#endif
+              if (!ok) break;
+            }
+            const uint8_t* src = smem + L::OffQSt + stage.slot * kStageBytes;
+            constexpr int kG = 256 / kConvThreads;
+            uint4 v[kG];
+            uint32_t sc[kG];
+            float ts[kG];
+#pragma unroll
+            for (int k = 0; k < kG; ++k) {
+              const int gi = k * kConvThreads + ct, r = gi >> 1, q = gi & 1;
+              v[k] = *reinterpret_cast<const uint4*>(src + r * 64 + (c & 1) * 32 + q * 16);
+              const uint8_t* ps = scl_b + tile_page(y_pages + (r >> 6)) * L::PageScl;
+              sc[k] = *reinterpret_cast<const uint16_t*>(ps + (r & 63) * 32 + 4 * c + 2 * q);
+              ts[k] = *reinterpret_cast<const float*>(ps + 2048 + (r & 63) * 4);
+            }
+#pragma unroll
+            for (int k = 0; k < kG; ++k) {
+              const int gi = k * kConvThreads + ct, r = gi >> 1, q = gi & 1;
+              uint4 o[4];
+              e2m1x32_scaled(v[k], sc[k], __float2half2_rn(ts[k]), o);
+              uint8_t* rp = dstu + r * 128;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(rp + (((4 * q + e) ^ (r & 7)) * 16)) = o[e];
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (c % kUnitsPerStage == kUnitsPerStage - 1) {
+              if (lane == 0) mbar_arrive_local(bar(L::QST_EMPTY + stage.slot));
+              stage.advance(L::QStSlots);
+            }
+          } else if (c < kChunks - 1) {
             // [2 pages][64 rows][64 codes]; the scale of columns [64c, 64c+64) is tile c/2
             ok = mbar_wait(bar(L::QST_FULL + stage.slot), stage.phase, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
@@ -924,7 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
         if (lane == 0) mbar_arrive_local(bar(L::SCL_EMPTY + (gt & 1)));
       }
     }
-  } else if (kFp8 && warp >= L::PVConvWarp && warp < L::PVConvWarp + L::ConvWarps) {
+  } else if (kConv && warp >= L::PVConvWarp && warp < L::PVConvWarp + L::ConvWarps) {
     // ------------------------------------------------- FP8: PV unit conversion
     const int ct = (warp - L::PVConvWarp) * 32 + lane;
     const int blk = (int)rank;  // + 2j: this CTA's 128 columns of half j are scale tile 2j + rank
@@ -940,7 +1038,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
         ok = mbar_wait(bar(L::SCL_FULL + (gt & 1)), (gt >> 1) & 1, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
         if (!ok) break;
-        const float* scl_t = reinterpret_cast<const float*>(smem + L::OffScl + (gt & 1) * kSclBytes);
+        const uint8_t* scl_b = smem + L::OffScl + (gt & 1) * L::SclBytes;
+        const float* scl_t = reinterpret_cast<const float*>(scl_b);
         const int pg0 = s.page_lo + it * kTilePages;
         const int npg = min(kTilePages, s.n_pages - it * kTilePages);
 #ifdef MLA_TC_TRACE
@@ -961,9 +1060,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
             w_unit += clock64() - tw;
             tw = clock64();
 #endif
-            ok = mbar_wait(bar(L::PST_FULL + stage.slot), stage.phase, abort_flag, p.status);
-            ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-            if (!ok) break;
+            if (j % kUnitsPerStage == 0) {
+              ok = mbar_wait(bar(L::PST_FULL + stage.slot), stage.phase, abort_flag, p.status);
+              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+              if (!ok) break;
+            }
 #ifdef MLA_TC_TRACE
             w_stage += clock64() - tw;
 #endif
@@ -974,6 +1075,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
 #endif
             // 64 rows x 128 codes -> two 64-column atoms (8 KB apart); rows
             // past the visible keys are zero
+            if constexpr (kFp4) {
+              // group gi: 32 columns (two blocks) of row (gi / 2) % 64, atom gi / 128
+              constexpr int kG = 256 / kConvThreads;
+              uint4 v[kG];
+              uint32_t sc[kG];
+              float ts[kG];
+              const uint8_t* ps = scl_b + tp * L::PageScl;
+#pragma unroll
+              for (int k = 0; k < kG; ++k) {
+                const int gi = k * kConvThreads + ct, row = (gi >> 1) & 63, q = gi & 1, atom = gi >> 7;
+                v[k] = make_uint4(0, 0, 0, 0);
+                sc[k] = 0;
+                ts[k] = 0.f;
+                if (row < valid) {
+                  v[k] = *reinterpret_cast<const uint4*>(src + j * 4096 + row * 64 + atom * 32 + q * 16);
+                  sc[k] = *reinterpret_cast<const uint16_t*>(ps + row * 32 + 16 * j + 8 * blk + 4 * atom + 2 * q);
+                  ts[k] = *reinterpret_cast<const float*>(ps + 2048 + row * 4);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < kG; ++k) {
+                const int gi = k * kConvThreads + ct, row = (gi >> 1) & 63, q = gi & 1, atom = gi >> 7;
+                uint4 o[4];
+                e2m1x32_scaled(v[k], sc[k], __float2half2_rn(ts[k]), o);
+                uint8_t* rp = dst + atom * 8192 + row * 128;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(rp + (((4 * q + e) ^ (row & 7)) * 16)) = o[e];
+              }
+            } else {
             constexpr int kG = 512 / kConvThreads;
             // all of the thread's codes and scales are loaded before any store
             uint4 v[kG];
@@ -1008,20 +1138,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
               *reinterpret_cast<uint4*>(rp + (((u0 + odd) ^ (row & 7)) * 16)) = odd ? od : ev;
               *reinterpret_cast<uint4*>(rp + (((u0 + 1 - odd) ^ (row & 7)) * 16)) = odd ? ev : od;
             }
+            }
 #ifdef MLA_TC_TRACE
             const long long tc1 = clock64();
             w_conv += tc1 - tc0;
 #endif
             fence_proxy_async();
             __syncwarp();
+            const bool staged_done = j % kUnitsPerStage == kUnitsPerStage - 1;
             if (lane == 0) {
-              mbar_arrive_local(bar(L::PST_EMPTY + stage.slot));
+              if (staged_done) mbar_arrive_local(bar(L::PST_EMPTY + stage.slot));
               mbar_arrive_cluster(leader_bar(L::PV_FULL + unit.slot));
             }
 #ifdef MLA_TC_TRACE
             w_fence += clock64() - tc1;
 #endif
-            stage.advance(L::PStSlots);
+            if (staged_done) stage.advance(L::PStSlots);
             unit.advance(L::PVSlots);
           }
         }
@@ -1060,7 +1192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
 #endif
           ok = mbar_wait(bar(L::S_FREE + (g & 1)), ((g >> 1) & 1) ^ 1, abort_flag, p.status);
 #ifdef MLA_TC_TRACE
-          if (!kFp8) TC_TRACE_VAL(11, g, clock64() - tq0);
+          if (!kConv) TC_TRACE_VAL(11, g, clock64() - tq0);
 #endif
           if (!ok) break;
           tc_fence_after();
@@ -1091,7 +1223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
           tc_commit_pair(bar(L::S_FULL + (g & 1)));
           TC_TRACE(1, g);
 #ifdef MLA_TC_TRACE
-          if (!kFp8) TC_TRACE_VAL(8, g, q_data);
+          if (!kConv) TC_TRACE_VAL(8, g, q_data);
 #endif
           if (g == 0) MLA_STAMP_ANY(4);
           if (it == n_tiles - 1) tc_commit_pair(bar(L::Q_EMPTY));
@@ -1121,7 +1253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
 #endif
           ok = mbar_wait(bar(L::P_FULL), g & 1, abort_flag, p.status);
 #ifdef MLA_TC_TRACE
-          if (!kFp8) TC_TRACE_VAL(10, g, clock64() - tp0);
+          if (!kConv) TC_TRACE_VAL(10, g, clock64() - tp0);
 #endif
           if (!ok) break;
           if (it == 0 && seg > 0) {  // O of the previous segment must be read out first
@@ -1153,7 +1285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
           tc_commit_pair(bar(L::O_DONE));
           TC_TRACE(3, g);
 #ifdef MLA_TC_TRACE
-          if (!kFp8) TC_TRACE_VAL(9, g, v_data);
+          if (!kConv) TC_TRACE_VAL(9, g, v_data);
 #endif
           if (g == 0) MLA_STAMP_ANY(6);
         }
@@ -1244,7 +1376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
             const float e0 = fast_exp2(__uint_as_float(sr[2 * j]) * p.scale_log2 - m_ref);
             const float e1 = fast_exp2(__uint_as_float(sr[2 * j + 1]) * p.scale_log2 - m_ref);
             PT h2;
-            if constexpr (kFp8) h2 = __floats2half2_rn(e0, e1);
+            if constexpr (kConv) h2 = __floats2half2_rn(e0, e1);
             else h2 = __floats2bfloat162_rn(e0, e1);
             s4[j & 1] += e0;
             s4[2 + (j & 1)] += e1;
@@ -1292,7 +1424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
           }
           return true;
         };
-        if constexpr (!kFp8) {
+        if constexpr (!kConv) {
           // the probabilities are formed while the previous PV runs; only
           // their stores into P wait for it
           uint32_t pk_lo[32], pk_hi[32];
@@ -1499,13 +1631,13 @@ bool make_o_map(CUtensorMap* m, void* base, uint64_t rows) {
          CUDA_SUCCESS;
 }
 
-template <bool kFp8>
+template <int kCache>
 cudaError_t launch_variant(const TcParams& tp, int pairs, cudaStream_t st) {
-  using L = TcLayout<kFp8>;
+  using L = TcLayout<kCache>;
   cudaError_t e =
-      cudaFuncSetAttribute(decode_tc_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SmemBytes);
+      cudaFuncSetAttribute(decode_tc_kernel<kCache>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_tc_kernel<kFp8>, dim3(2 * pairs), dim3(L::Threads), L::SmemBytes, st, tp);
+  e = launch_pdl(decode_tc_kernel<kCache>, dim3(2 * pairs), dim3(L::Threads), L::SmemBytes, st, tp);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1513,11 +1645,11 @@ cudaError_t launch_variant(const TcParams& tp, int pairs, cudaStream_t st) {
 
 bool decode_tc_supported(const mla_dims& d, int n_q) {
   return d.n_heads == kHeads && d.d_c == kDC && d.d_rope == kDR && d.page_size == kPage &&
-         d.act_dtype == MLA_BF16 && (d.cache_dtype == MLA_BF16 || d.cache_dtype == MLA_FP8_E4M3) && n_q >= 1 &&
+         d.act_dtype == MLA_BF16 && (d.cache_dtype == MLA_BF16 || is_coded_cache(d)) && n_q >= 1 &&
          n_q <= 8 && device_is_sm100();
 }
 
-bool decode_tc_wants_f16_queries(const mla_dims& d) { return d.cache_dtype == MLA_FP8_E4M3; }
+bool decode_tc_wants_f16_queries(const mla_dims& d) { return is_coded_cache(d); }
 
 int decode_tc_auto_splits(int num_sms, int n_q) {
   const int pairs = num_sms / 2;
@@ -1529,10 +1661,21 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st) {
   TcParams tp;
   memset(&tp, 0, sizeof(tp));
   tp.p = p;
-  const bool fp8 = p.d.cache_dtype == MLA_FP8_E4M3;
   const uint64_t q_rows = (uint64_t)p.batch * p.n_q * kHeads;
   if (!make_o_map(&tp.map_o, p.o_part, (uint64_t)p.n_q * p.n_slots * kHeads)) return cudaErrorInvalidValue;
-  if (fp8) {
+  if (p.d.cache_dtype == MLA_FP4_E2M1) {
+    const Fp4Page f4 = fp4_page(kPage, kDC, kDR);
+    tp.scl_off = f4.sc_off;
+    if (!make_map(&tp.map_q, p.q_abs, q_rows, 64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) ||
+        !make_page_map(&tp.map_codes_pv, p.pool, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kDC / 2, p.num_pages, p.page_bytes,
+                       64) ||
+        !make_page_map(&tp.map_kr, p.pool + f4.kr_off, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kDR, p.num_pages,
+                       p.page_bytes, 64))
+      return cudaErrorInvalidValue;
+    tp.map_codes_qk = tp.map_codes_pv;
+    return launch_variant<MLA_FP4_E2M1>(tp, p.splits * p.n_q, st);
+  }
+  if (p.d.cache_dtype == MLA_FP8_E4M3) {
     const Fp8Page fp = fp8_page(kPage, kDC, kDR);
     if (!make_map(&tp.map_q, p.q_abs, q_rows, 64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) ||
         !make_page_map(&tp.map_codes_qk, p.pool, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kDC, p.num_pages, p.page_bytes,
@@ -1544,13 +1687,13 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st) {
         !make_page_map(&tp.map_scl, p.pool + fp.sc_off, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, kDC / 128, p.num_pages,
                        p.page_bytes, kDC / 128))
       return cudaErrorInvalidValue;
-    return launch_variant<true>(tp, p.splits * p.n_q, st);
+    return launch_variant<MLA_FP8_E4M3>(tp, p.splits * p.n_q, st);
   }
   const uint64_t pool_rows = (uint64_t)p.num_pages * kPage;
   if (!make_map(&tp.map_q, p.q_abs, q_rows, 64) || !make_map(&tp.map_pv, p.pool, pool_rows, 64) ||
       !make_map(&tp.map_pv16, p.pool, pool_rows, 16) || !make_map(&tp.map_row, p.pool, pool_rows, 1))
     return cudaErrorInvalidValue;
-  return launch_variant<false>(tp, p.splits * p.n_q, st);
+  return launch_variant<MLA_BF16>(tp, p.splits * p.n_q, st);
 }
 
 }  // namespace mla

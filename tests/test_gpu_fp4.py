@@ -135,3 +135,98 @@ def test_step_rows_append_attend_and_read_together(heads):
     side.synchronize()
     assert torch.equal(gp.session.out, first)
     assert gp.status() == 0
+
+
+# lengths before the step around pages (64), tiles (256) and splits
+RAGGED = (0, 1, 62, 63, 64, 65, 127, 128, 254, 255, 256, 257, 700, 1500)
+
+
+@pytest.mark.parametrize("heads", [128])
+@pytest.mark.parametrize("T", [1, 2, 3, 8])
+@pytest.mark.parametrize("num_splits", [0, 1, 7])
+def test_tensor_core_ragged(heads, T, num_splits):
+    check(fp4_cfg(n_heads=heads, B=len(RAGGED), T=T, L=RAGGED), num_splits=num_splits, path=1)
+
+
+@pytest.mark.parametrize("heads", [128])
+def test_tensor_core_long(heads):
+    check(fp4_cfg(n_heads=heads, B=1, T=2, L=(9000,)), path=1)
+
+
+@pytest.mark.parametrize("heads", [128])
+def test_rows_behind_the_end_do_not_reach_the_output(heads):
+    """Everything past a sequence's last key, in its last page and in pages no
+    sequence holds, is NaN (codes, scales, token scales and k^R): the outputs are those
+    of a clean pool, bit for bit."""
+    cfg = fp4_cfg(n_heads=heads, B=5, T=2, L=(0, 5, 62, 300, 1000), spare_pages=3)
+    gp = GpuProblem(cfg)
+    out, lse = gp.run()
+    ref, ref_lse = out.clone(), lse.clone()
+    v = gp.cache.views()
+    keep = torch.zeros(cfg.num_pages, 64, dtype=torch.bool)
+    for b, n in enumerate(cfg.seq_lens):
+        pos = np.arange(n)
+        keep[gp.pt_host[b, pos // 64], pos % 64] = True
+    bad = ~keep.cuda()
+    v["scales"][bad] = 0x7F
+    v["ts"][bad] = float("nan")
+    v["kr"][bad] = float("inf")
+    v["codes"][bad] = 0xFF
+    out, lse = gp.run()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    assert gp.status() == 0
+
+
+@pytest.mark.parametrize("heads", [128])
+def test_deterministic_and_page_order_invariant(heads):
+    cfg = fp4_cfg(n_heads=heads, B=3, T=2, L=(100, 777, 2000))
+    gp = GpuProblem(cfg)
+    out, lse = gp.run()
+    ref, ref_lse = out.clone(), lse.clone()
+    for _ in range(3):
+        out, lse = gp.run()
+        assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    other = GpuProblem(cfg, page_table=W.page_table(cfg, seed_offset=5))
+    out, lse = other.run()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+@pytest.mark.parametrize("heads", [128])
+def test_bad_pages_and_short_sequences_are_reported(heads):
+    cfg = fp4_cfg(n_heads=heads, B=3, T=2, L=(100, 300, 500))
+    gp = GpuProblem(cfg)
+    out, _ = gp.run()
+    ref = out.clone()
+    table = gp.page_table.clone()
+    table[1, 2] = cfg.num_pages + 7
+    i = gp.inputs
+    out, _ = gp.session.attend(i["q_nope"], i["q_rope"], gp.weights["W_uk"], gp.weights["W_uv"], gp.cache.pool, table,
+                               gp.seq_lens)
+    torch.cuda.synchronize()
+    assert gp.status() == B.MLA_ERR_BOUNDS
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[2], ref[2])
+    lens = gp.seq_lens.clone()
+    lens[1] = 1  # shorter than the two new tokens: no key for this sequence
+    out, lse = gp.session.attend(i["q_nope"], i["q_rope"], gp.weights["W_uk"], gp.weights["W_uv"], gp.cache.pool,
+                                 gp.page_table, lens)
+    torch.cuda.synchronize()
+    assert gp.status() == B.MLA_ERR_BOUNDS
+    assert (out[1] == 0).all() and torch.isinf(lse[1]).all()
+    assert rel_err(out[0].double().cpu().numpy(), ref[0].double().cpu().numpy()) < 1e-2
+    assert rel_err(out[2].double().cpu().numpy(), ref[2].double().cpu().numpy()) < 1e-2
+
+
+@pytest.mark.parametrize("heads", [128])
+def test_expired_wait_is_reported_and_the_next_step_is_right(heads):
+    """With the self-test flag the load producers issue no load: the bounded waits expire."""
+    cfg = fp4_cfg(n_heads=heads, B=2, T=1, L=(100, 300))
+    gp = GpuProblem(cfg)
+    ref = gp.run()[0].clone()
+    gp.session.dims = B.dims_for(cfg, B.MLA_FLAG_SELFTEST_STALL)
+    i = gp.inputs
+    B.mla_decode(gp.session.dims, i["q_nope"], i["q_rope"], gp.weights["W_uk"], gp.cache.pool, gp.page_table,
+                 gp.seq_lens, gp.session.decode_ws)
+    assert gp.status() == B.MLA_ERR_TIMEOUT
+    gp.session.dims = gp.dims
+    assert torch.equal(gp.run()[0], ref)
+    assert gp.status() == 0
