@@ -91,16 +91,23 @@ struct TcLayout {
   static constexpr bool kConv = kCache != MLA_BF16;       // converter warps write the operand units
   static constexpr bool kFp4 = kCache == MLA_FP4_E2M1;
   static constexpr int QKSlots = kConv ? 2 : 3, PVSlots = kConv ? 2 : 4;
-  static constexpr int QStSlots = kFp4 ? 2 : kConv ? 3 : 0, PStSlots = QStSlots;
-  static constexpr int SclBufs = kConv ? 2 : 0;  // per-tile scales of the four pages
-  static constexpr uint32_t PageScl = kPageScl<kCache>, SclBytes = kTilePages * PageScl;
+  static constexpr int QStSlots = kConv ? 3 : 0, PStSlots = kFp4 ? 2 : QStSlots;
+  // Scales: FP8 keeps a tile's four pages in one block that both rings'
+  // converters share.  4-bit rows carry twice the scale bytes, and a shared
+  // block would tie the QK units of tile g + 2 to the PV units of tile g
+  // (measured: 7.8 us a tile, 1.9 ms on 128 sequences of 16,384 with two
+  // tokens): the QK block holds this CTA's two pages, and a PV staging slot
+  // brings its page's scales along.
+  static constexpr int SclBufs = kConv ? 2 : 0, SclPages = kFp4 ? 2 : kTilePages;
+  static constexpr uint32_t PageScl = kPageScl<kCache>, SclBytes = SclPages * PageScl;
+  static constexpr uint32_t PStBytes = kStageBytes + (kFp4 ? PageScl : 0);
   static constexpr uint32_t OffQ = 0;
   static constexpr uint32_t OffP = OffQ + kQBytes;
   static constexpr uint32_t OffQKRing = OffP + kPBytes;
   static constexpr uint32_t OffPVRing = OffQKRing + QKSlots * kUnitBytes;
   static constexpr uint32_t OffQSt = OffPVRing + PVSlots * kUnitBytes;
   static constexpr uint32_t OffPSt = OffQSt + QStSlots * kStageBytes;
-  static constexpr uint32_t OffScl = OffPSt + PStSlots * kStageBytes;
+  static constexpr uint32_t OffScl = OffPSt + PStSlots * PStBytes;
   static constexpr uint32_t OffBar = OffScl + SclBufs * SclBytes;
   // barrier indices
   static constexpr int QK_FULL = 0;                     // [QKSlots] leader: unit written in both CTAs
@@ -409,12 +416,17 @@ __device__ __forceinline__ void e4m3x4_scaled(uint32_t w, __half2 s2, uint32_t& 
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// 32 e2m1 codes (16 bytes: two blocks of 16 columns) times their scales -> 64
-// bytes of f16.  s: the blocks' e4m3 scales, the first in the low byte; ts: the
-// token's scale.
-__device__ __forceinline__ void e2m1x32_scaled(const uint4& w, uint32_t s, __half2 ts, uint4 (&o)[4]) {
-  const __half2 sc = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)s, __NV_E4M3)), ts);
-  const __half2 s0 = __low2half2(sc), s1 = __high2half2(sc);
+// Scales of 32 columns (two blocks) as f16 pairs: e4m3 block scales (low byte
+// first) times the token's scale.
+__device__ __forceinline__ void fp4_block_scales(uint32_t sc, __half2 ts, __half2& s0, __half2& s1) {
+  const __half2 s = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)sc, __NV_E4M3)), ts);
+  s0 = __low2half2(s);
+  s1 = __high2half2(s);
+}
+
+// 32 e2m1 codes (two blocks of 16 columns) times their scales -> 64 bytes of
+// f16: the 16-byte units u0 ^ e, e = 0..3, of a 128-byte swizzled row.
+__device__ __forceinline__ void store_e2m1x32(uint8_t* row, uint32_t u0, const uint4& w, __half2 s0, __half2 s1) {
   const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -426,7 +438,7 @@ __device__ __forceinline__ void e2m1x32_scaled(const uint4& w, uint32_t s, __hal
       const __half2 v = __hmul2(h[e], i < 2 ? s0 : s1);
       r[e] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    o[i] = make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4*>(row + ((u0 ^ i) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
@@ -651,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
     }
     for (int i = 0; i < L::SclBufs; ++i) {
       mbar_init(bar(L::SCL_FULL + i), 1);
-      mbar_init(bar(L::SCL_EMPTY + i), 2 * L::ConvWarps);
+      mbar_init(bar(L::SCL_EMPTY + i), (kFp4 ? 1 : 2) * L::ConvWarps);
     }
     mbar_init(bar(L::DRAIN), 2);  // the QK and the PV issuer's final commit
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -689,611 +701,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
   // Self-test of failure detection: no producer issues a load, so the MMA
   // issuers' and softmax warps' bounded waits expire with no copy in flight.
   const bool stall = (p.d.flags & MLA_FLAG_SELFTEST_STALL) != 0;
-  if (warp >= L::QKProdWarp && warp < L::QKProdWarp + L::Producers) {
-    // -------------------------------------------------------------- TMA: Q, QK
-    if (lane == 0 && !stall) {
-      const int pid = warp - L::QKProdWarp;
-      RingProducer ring{kConv ? L::QStSlots : L::QKSlots, L::Producers, pid};
-      const uint32_t empty0 = kConv ? bar(L::QST_EMPTY) : bar(L::QK_EMPTY);
-      const int y_pages = 2 * (int)rank;  // this CTA's key positions of a tile (pages tile_page(...))
-      SegmentWalker walk(p, w, t);
-      Segment s;
-      uint32_t seg = 0, gtile = 0;
-      bool ok = true;
-      while (ok && walk.next(s)) {
-        if (s.n_pages == 0) continue;
-        // absorbed queries of this CTA's 64 heads for (b, t)
-        if (pid == 0) {
-          if (seg > 0) ok = mbar_wait(bar(L::Q_EMPTY), (seg - 1) & 1, abort_flag, p.status);
-          if (!ok) break;
-          // one barrier per 64-column chunk: the first tile's MMAs of unit c
-          // wait only for chunk c
-          if (rank == 0)
-            for (int c = 0; c < kChunks; ++c) mbar_expect_tx(bar(L::Q_FULL + c), 2 * 8192);
-          const int qrow = ((s.b * p.n_q + t) * kHeads) + kHalfHeads * (int)rank;
-          for (int c = 0; c < kChunks; ++c)
-            tma_load_2d_pair(sbase + L::OffQ + c * 8192, &P.map_q, 64 * c, qrow, leader_bar(L::Q_FULL + c));
-        }
-        const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
-        for (int it = 0; it < n_tiles && ok; ++it) {
-          const int pg0 = s.page_lo + it * kTilePages;
-          const int npg = min(kTilePages, s.n_pages - it * kTilePages);
-          // this CTA's pages; pages past the tile's end come from outside the
-          // tensor (zero fill)
-          int pg[2];
-          for (int i = 0; i < 2; ++i) {
-            const int tp = tile_page(y_pages + i);
-            pg[i] = tp < npg ? page_of(s.b, pg0 + tp) : -1;
-          }
-          if constexpr (kConv) {
-            // this CTA's pages two tiles ahead (at a segment's start also one
-            // ahead) go to L2 now, so that the staging loads find them there.
-            // (Measured: a gain for the FP8 cache, whose converters bound the
-            // tile; a loss for bf16, whose ring loads wait behind the bulk
-            // prefetches in the TMA unit.)  Invalid entries are skipped here
-            // and reported when their tile is loaded.
-            if (pid == 0) {
-              for (int d = it == 0 ? 1 : 2; d <= 2 && it + d < n_tiles; ++d) {
-                const int pgp = s.page_lo + (it + d) * kTilePages;
-                const int npgp = min(kTilePages, s.n_pages - (it + d) * kTilePages);
-                for (int i = 0; i < 2; ++i) {
-                  const int tp = tile_page(y_pages + i);
-                  if (tp >= npgp) continue;
-                  const int page = p.page_table[(size_t)s.b * p.max_pages + pgp + tp];
-                  if (page >= 0 && page < p.num_pages)
-                    prefetch_l2(p.pool + (size_t)page * p.page_bytes, (uint32_t)p.page_bytes);
-                }
-              }
-            }
-            // scales of the tile's four pages (zero for pages past its end)
-            if (pid == 0) {
-              const uint32_t sb = gtile & 1;
-              ok = mbar_wait(bar(L::SCL_EMPTY + sb), ((gtile >> 1) & 1) ^ 1, abort_flag, p.status);
-              if (!ok) break;
-              const uint32_t fb = bar(L::SCL_FULL + sb);
-              mbar_arrive_tx_local(fb, L::SclBytes);
-              for (int i = 0; i < kTilePages; ++i) {
-                const uint32_t dst = sbase + L::OffScl + sb * L::SclBytes + i * L::PageScl;
-                if constexpr (kFp4)  // (a page past the tile's end: the first page's scales, which nothing uses)
-                  bulk_load(dst, p.pool + (size_t)page_of(s.b, pg0 + (i < npg ? i : 0)) * p.page_bytes + P.scl_off,
-                            L::PageScl, fb);
-                else
-                  tma_load_3d(dst, &P.map_scl, 0, 0, i < npg ? page_of(s.b, pg0 + i) : -1, fb);
-              }
-            }
-            ++gtile;
-          }
-          for (int c = 0; c < kQKUnits; ++c) {
-            if constexpr (!kConv) {
-              uint32_t slot;
-              if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
-              if (rank == 0) mbar_expect_tx(bar(L::QK_FULL + slot), 2 * kUnitBytes);
-              const uint32_t dst = sbase + L::OffQKRing + slot * kUnitBytes, fb = leader_bar(L::QK_FULL + slot);
-              for (int i = 0; i < 2; ++i)
-                tma_load_2d_pair(dst + i * 8192, &P.map_pv, 64 * c, pg[i] >= 0 ? pg[i] * kPage : -kPage, fb);
-            } else if (c < kChunks - 1) {
-              // codes of columns [64c, 64c+64) of both pages (4-bit: of 128
-              // columns, for two units): one staging slot
-              if (c % kUnitsPerStage != 0) continue;
-              uint32_t slot;
-              if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
-              const uint32_t dst = sbase + L::OffQSt + slot * kStageBytes, fb = bar(L::QST_FULL + slot);
-              mbar_arrive_tx_local(fb, kStageBytes);
-              for (int i = 0; i < 2; ++i)
-                tma_load_3d(dst + i * 4096, &P.map_codes_qk, kFp4 ? 32 * c : 64 * c, 0, pg[i], fb);
-            } else {
-              // k^R: one staging slot per page
-              for (int i = 0; i < 2; ++i) {
-                uint32_t slot;
-                if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
-                const uint32_t dst = sbase + L::OffQSt + slot * kStageBytes, fb = bar(L::QST_FULL + slot);
-                mbar_arrive_tx_local(fb, kStageBytes);
-                tma_load_3d(dst, &P.map_kr, 0, 0, pg[i], fb);
-              }
-            }
-          }
-        }
-        ++seg;
-      }
-    }
-  } else if (warp >= L::PVProdWarp && warp < L::PVProdWarp + L::Producers) {
-    // ------------------------------------------------------------------ TMA: PV
-    if (lane == 0 && !stall) {
-      RingProducer ring{kConv ? L::PStSlots : L::PVSlots, L::Producers, warp - L::PVProdWarp};
-      const uint32_t empty0 = kConv ? bar(L::PST_EMPTY) : bar(L::PV_EMPTY);
-      const int x_pv = 128 * (int)rank;  // this CTA's 128 columns of an N=256 half
-      SegmentWalker walk(p, w, t);
-      Segment s;
-      bool ok = true;
-      while (ok && walk.next(s)) {
-        if (s.n_pages == 0) continue;
-        const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
-        for (int it = 0; it < n_tiles && ok; ++it) {
-          const int pg0 = s.page_lo + it * kTilePages;
-          const int npg = min(kTilePages, s.n_pages - it * kTilePages);
-          // key position i outer (page tile_page(i)), N-half j inner
-          for (int i = 0; i < kTilePages; ++i) {
-            const int tp = tile_page(i);
-            const int valid = tp < npg ? min(kPage, s.nvis - (pg0 + tp) * kPage) : 0;
-            const int page = valid > 0 ? page_of(s.b, pg0 + tp) : 0;
-            for (int j = 0; j < 2; ++j) {
-              if (kFp4 && j == 1) break;  // one slot holds both halves' codes
-              uint32_t slot;
-              if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
-              const int x0 = 256 * j + x_pv;
-              if constexpr (kFp4) {
-                const uint32_t fb = bar(L::PST_FULL + slot);
-                mbar_arrive_tx_local(fb, kStageBytes);
-                for (int jj = 0; jj < 2; ++jj)
-                  tma_load_3d(sbase + L::OffPSt + slot * kStageBytes + jj * 4096, &P.map_codes_pv, (256 * jj + x_pv) / 2,
-                              0, valid > 0 ? page : -1, fb);
-              } else if constexpr (kConv) {
-                // the converters zero the rows past the visible keys
-                const uint32_t fb = bar(L::PST_FULL + slot);
-                mbar_arrive_tx_local(fb, kStageBytes);
-                tma_load_3d(sbase + L::OffPSt + slot * kStageBytes, &P.map_codes_pv, x0, 0, valid > 0 ? page : -1, fb);
-              } else {
-                // Rows past the visible keys and pages past the tile's end
-                // come from outside the tensor (zero fill), so 0 * (whatever
-                // the pool held) cannot reach O.
-                if (rank == 0) mbar_expect_tx(bar(L::PV_FULL + slot), 2 * kUnitBytes);
-                const uint32_t dst = sbase + L::OffPVRing + slot * kUnitBytes, fb = leader_bar(L::PV_FULL + slot);
-                for (int a = 0; a < 2; ++a) {
-                  const int x = x0 + 64 * a;
-                  const uint32_t d = dst + a * 8192;
-                  if (valid == kPage) {
-                    tma_load_2d_pair(d, &P.map_pv, x, page * kPage, fb);
-                  } else if (valid <= 0) {
-                    tma_load_2d_pair(d, &P.map_pv, x, -kPage, fb);
-                  } else {
-                    for (int q = 0; q < 4; ++q) {
-                      if (16 * q + 16 <= valid) {
-                        tma_load_2d_pair(d + q * 2048, &P.map_pv16, x, page * kPage + 16 * q, fb);
-                      } else if (16 * q >= valid) {
-                        tma_load_2d_pair(d + q * 2048, &P.map_pv16, x, -16, fb);
-                      } else {
-                        for (int k = 0; k < 16; ++k)
-                          tma_load_2d_pair(d + (16 * q + k) * 128, &P.map_row, x,
-                                           16 * q + k < valid ? page * kPage + 16 * q + k : -1, fb);
-                      }
-                    }
-                  }
-                }
-              }
-            }
-          }
-        }
-      }
-    }
-  } else if (kConv && warp >= L::QKConvWarp && warp < L::QKConvWarp + L::ConvWarps) {
-    // ------------------------------------------------- FP8: QK unit conversion
-    // Thread ct of the converter warps converts 16-byte groups ct,
-    // ct + kConvThreads, ... of the staged data into the unit (128-byte swizzle).
-    const int ct = (warp - L::QKConvWarp) * 32 + lane;
-    RingPos unit, stage;
-    uint32_t gt = 0;
-    const int y_pages = 2 * (int)rank;
-    SegmentWalker walk(p, w, t);
-    Segment s;
-    bool ok = true;
-    while (ok && walk.next(s)) {
-      if (s.n_pages == 0) continue;
-      const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
-      for (int it = 0; it < n_tiles && ok; ++it, ++gt) {
-        ok = mbar_wait(bar(L::SCL_FULL + (gt & 1)), (gt >> 1) & 1, abort_flag, p.status);
-        ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-        if (!ok) break;
-        // the tile's scales, [4 pages][64 rows][4 tiles of 128 columns]
-        const uint8_t* scl_b = smem + L::OffScl + (gt & 1) * L::SclBytes;
-        const float* scl = reinterpret_cast<const float*>(scl_b);
-#ifdef MLA_TC_TRACE
-        long long w_unit = 0, w_stage = 0, t_tile = clock64();
-#endif
-        for (int c = 0; c < kQKUnits && ok; ++c) {
-#ifdef MLA_TC_TRACE
-          long long tw = clock64();
-#endif
-          ok = mbar_wait(bar(L::QK_EMPTY + unit.slot), unit.phase ^ 1, abort_flag, p.status);
-          ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-#ifdef MLA_TC_TRACE
-          w_unit += clock64() - tw;
-          tw = clock64();
-#endif
-          if (!ok) break;
-          uint8_t* dstu = smem + L::OffQKRing + unit.slot * kUnitBytes;
-          if (kFp4 && c < kChunks - 1) {
-            // [2 pages][64 rows][128 codes], this unit's 64 of them: group gi is
-            // 32 columns (two blocks) of unit row gi / 2
-            if (c % kUnitsPerStage == 0) {
-              ok = mbar_wait(bar(L::QST_FULL + stage.slot), stage.phase, abort_flag, p.status);
-              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-#ifdef MLA_TC_TRACE
-              w_stage += clock64() - tw;
-#endif
-              if (!ok) break;
-            }
-            const uint8_t* src = smem + L::OffQSt + stage.slot * kStageBytes;
-            constexpr int kG = 256 / kConvThreads;
-            uint4 v[kG];
-            uint32_t sc[kG];
-            float ts[kG];
-#pragma unroll
-            for (int k = 0; k < kG; ++k) {
-              const int gi = k * kConvThreads + ct, r = gi >> 1, q = gi & 1;
-              v[k] = *reinterpret_cast<const uint4*>(src + r * 64 + (c & 1) * 32 + q * 16);
-              const uint8_t* ps = scl_b + tile_page(y_pages + (r >> 6)) * L::PageScl;
-              sc[k] = *reinterpret_cast<const uint16_t*>(ps + (r & 63) * 32 + 4 * c + 2 * q);
-              ts[k] = *reinterpret_cast<const float*>(ps + 2048 + (r & 63) * 4);
-            }
-#pragma unroll
-            for (int k = 0; k < kG; ++k) {
-              const int gi = k * kConvThreads + ct, r = gi >> 1, q = gi & 1;
-              uint4 o[4];
-              e2m1x32_scaled(v[k], sc[k], __float2half2_rn(ts[k]), o);
-              uint8_t* rp = dstu + r * 128;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(rp + (((4 * q + e) ^ (r & 7)) * 16)) = o[e];
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (c % kUnitsPerStage == kUnitsPerStage - 1) {
-              if (lane == 0) mbar_arrive_local(bar(L::QST_EMPTY + stage.slot));
-              stage.advance(L::QStSlots);
-            }
-          } else if (c < kChunks - 1) {
-            // [2 pages][64 rows][64 codes]; the scale of columns [64c, 64c+64) is tile c/2
-            ok = mbar_wait(bar(L::QST_FULL + stage.slot), stage.phase, abort_flag, p.status);
-            ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-#ifdef MLA_TC_TRACE
-            w_stage += clock64() - tw;
-#endif
-            if (!ok) break;
-            const uint8_t* src = smem + L::OffQSt + stage.slot * kStageBytes;
-            constexpr int kG = 512 / kConvThreads;  // 16-byte groups per thread
-            // all of the thread's codes and scales are loaded before any store
-            uint4 v[kG];
-            float sc[kG];
-#pragma unroll
-            for (int k = 0; k < kG; ++k) {
-              const int gi = k * kConvThreads + ct, r = gi >> 2, q = gi & 3;  // r: unit row (this CTA's page r/64)
-              v[k] = *reinterpret_cast<const uint4*>(src + r * 64 + q * 16);
-              sc[k] = scl[(tile_page(y_pages + (r >> 6)) * 64 + (r & 63)) * 4 + (c >> 1)];
-            }
-#pragma unroll
-            for (int k = 0; k < kG; ++k) {
-              const int gi = k * kConvThreads + ct, r = gi >> 2, q = gi & 3;
-              const __half2 s2 = __float2half2_rn(sc[k]);
-              uint32_t o[8];
-              e4m3x4_scaled(v[k].x, s2, o[0], o[1]);
-              e4m3x4_scaled(v[k].y, s2, o[2], o[3]);
-              e4m3x4_scaled(v[k].z, s2, o[4], o[5]);
-              e4m3x4_scaled(v[k].w, s2, o[6], o[7]);
-              uint8_t* rp = dstu + r * 128;
-              *reinterpret_cast<uint4*>(rp + (((2 * q) ^ (r & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(rp + (((2 * q + 1) ^ (r & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_local(bar(L::QST_EMPTY + stage.slot));
-            stage.advance(L::QStSlots);
-          } else {
-            // k^R: one staged page (64 rows x 64 bf16) per half of the unit
-            for (int i = 0; i < 2 && ok; ++i) {
-              ok = mbar_wait(bar(L::QST_FULL + stage.slot), stage.phase, abort_flag, p.status);
-              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-              if (!ok) break;
-              const uint8_t* src = smem + L::OffQSt + stage.slot * kStageBytes;
-              uint8_t* dst = dstu + i * 8192;
-              constexpr int kG = 512 / kConvThreads;
-              uint4 v[kG];
-#pragma unroll
-              for (int k = 0; k < kG; ++k) {
-                const int gi = k * kConvThreads + ct, row = gi >> 3, u = gi & 7;
-                v[k] = *reinterpret_cast<const uint4*>(src + row * 128 + u * 16);
-              }
-#pragma unroll
-              for (int k = 0; k < kG; ++k) {
-                const int gi = k * kConvThreads + ct, row = gi >> 3, u = gi & 7;
-                *reinterpret_cast<uint4*>(dst + row * 128 + ((u ^ (row & 7)) * 16)) =
-                    make_uint4(bf16x2_to_f16x2(v[k].x), bf16x2_to_f16x2(v[k].y), bf16x2_to_f16x2(v[k].z),
-                               bf16x2_to_f16x2(v[k].w));
-              }
-              fence_proxy_async();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_local(bar(L::QST_EMPTY + stage.slot));
-              stage.advance(L::QStSlots);
-            }
-            if (!ok) break;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(leader_bar(L::QK_FULL + unit.slot));
-          unit.advance(L::QKSlots);
-        }
-        if (!ok) break;
-#ifdef MLA_TC_TRACE
-        if (ct == 0) {
-          TC_TRACE_VAL(8, gt, w_unit);
-          TC_TRACE_VAL(9, gt, w_stage);
-          TC_TRACE_VAL(10, gt, clock64() - t_tile);
-          TC_TRACE(11, gt);
-        }
-#endif
-        __syncwarp();
-        if (lane == 0) mbar_arrive_local(bar(L::SCL_EMPTY + (gt & 1)));
-      }
-    }
-  } else if (kConv && warp >= L::PVConvWarp && warp < L::PVConvWarp + L::ConvWarps) {
-    // ------------------------------------------------- FP8: PV unit conversion
-    const int ct = (warp - L::PVConvWarp) * 32 + lane;
-    const int blk = (int)rank;  // + 2j: this CTA's 128 columns of half j are scale tile 2j + rank
-    RingPos unit, stage;
-    uint32_t gt = 0;
-    SegmentWalker walk(p, w, t);
-    Segment s;
-    bool ok = true;
-    while (ok && walk.next(s)) {
-      if (s.n_pages == 0) continue;
-      const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
-      for (int it = 0; it < n_tiles && ok; ++it, ++gt) {
-        ok = mbar_wait(bar(L::SCL_FULL + (gt & 1)), (gt >> 1) & 1, abort_flag, p.status);
-        ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-        if (!ok) break;
-        const uint8_t* scl_b = smem + L::OffScl + (gt & 1) * L::SclBytes;
-        const float* scl_t = reinterpret_cast<const float*>(scl_b);
-        const int pg0 = s.page_lo + it * kTilePages;
-        const int npg = min(kTilePages, s.n_pages - it * kTilePages);
-#ifdef MLA_TC_TRACE
-        long long w_unit = 0, w_stage = 0, w_conv = 0, w_fence = 0, t_tile = clock64();
-#endif
-        for (int i = 0; i < kTilePages && ok; ++i) {
-          const int tp = tile_page(i);
-          const int valid = tp < npg ? min(kPage, s.nvis - (pg0 + tp) * kPage) : 0;
-          const float* scl = scl_t + tp * 256;
-          for (int j = 0; j < 2 && ok; ++j) {
-#ifdef MLA_TC_TRACE
-            long long tw = clock64();
-#endif
-            ok = mbar_wait(bar(L::PV_EMPTY + unit.slot), unit.phase ^ 1, abort_flag, p.status);
-            ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-            if (!ok) break;
-#ifdef MLA_TC_TRACE
-            w_unit += clock64() - tw;
-            tw = clock64();
-#endif
-            if (j % kUnitsPerStage == 0) {
-              ok = mbar_wait(bar(L::PST_FULL + stage.slot), stage.phase, abort_flag, p.status);
-              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-              if (!ok) break;
-            }
-#ifdef MLA_TC_TRACE
-            w_stage += clock64() - tw;
-#endif
-            const uint8_t* src = smem + L::OffPSt + stage.slot * kStageBytes;
-            uint8_t* dst = smem + L::OffPVRing + unit.slot * kUnitBytes;
-#ifdef MLA_TC_TRACE
-            const long long tc0 = clock64();
-#endif
-            // 64 rows x 128 codes -> two 64-column atoms (8 KB apart); rows
-            // past the visible keys are zero
-            if constexpr (kFp4) {
-              // group gi: 32 columns (two blocks) of row (gi / 2) % 64, atom gi / 128
-              constexpr int kG = 256 / kConvThreads;
-              uint4 v[kG];
-              uint32_t sc[kG];
-              float ts[kG];
-              const uint8_t* ps = scl_b + tp * L::PageScl;
-#pragma unroll
-              for (int k = 0; k < kG; ++k) {
-                const int gi = k * kConvThreads + ct, row = (gi >> 1) & 63, q = gi & 1, atom = gi >> 7;
-                v[k] = make_uint4(0, 0, 0, 0);
-                sc[k] = 0;
-                ts[k] = 0.f;
-                if (row < valid) {
-                  v[k] = *reinterpret_cast<const uint4*>(src + j * 4096 + row * 64 + atom * 32 + q * 16);
-                  sc[k] = *reinterpret_cast<const uint16_t*>(ps + row * 32 + 16 * j + 8 * blk + 4 * atom + 2 * q);
-                  ts[k] = *reinterpret_cast<const float*>(ps + 2048 + row * 4);
-                }
-              }
-#pragma unroll
-              for (int k = 0; k < kG; ++k) {
-                const int gi = k * kConvThreads + ct, row = (gi >> 1) & 63, q = gi & 1, atom = gi >> 7;
-                uint4 o[4];
-                e2m1x32_scaled(v[k], sc[k], __float2half2_rn(ts[k]), o);
-                uint8_t* rp = dst + atom * 8192 + row * 128;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(rp + (((4 * q + e) ^ (row & 7)) * 16)) = o[e];
-              }
-            } else {
-            constexpr int kG = 512 / kConvThreads;
-            // all of the thread's codes and scales are loaded before any store
-            uint4 v[kG];
-            float sc[kG];
-#pragma unroll
-            for (int k = 0; k < kG; ++k) {
-              const int gi = k * kConvThreads + ct, row = gi >> 3, q = gi & 7;
-              v[k] = make_uint4(0, 0, 0, 0);
-              sc[k] = 0.f;
-              if (row < valid) {
-                v[k] = *reinterpret_cast<const uint4*>(src + row * 128 + q * 16);
-                sc[k] = scl[row * 4 + 2 * j + blk];
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < kG; ++k) {
-              const int gi = k * kConvThreads + ct, row = gi >> 3, q = gi & 7;
-              uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-              if (row < valid) {
-                const __half2 s2 = __float2half2_rn(sc[k]);
-                e4m3x4_scaled(v[k].x, s2, o[0], o[1]);
-                e4m3x4_scaled(v[k].y, s2, o[2], o[3]);
-                e4m3x4_scaled(v[k].z, s2, o[4], o[5]);
-                e4m3x4_scaled(v[k].w, s2, o[6], o[7]);
-              }
-              // the eight threads of a row cover both 64-column atoms; threads
-              // of the second atom store their odd unit first, so the two
-              // stores of each phase fall on distinct banks
-              uint8_t* rp = dst + (q >> 2) * 8192 + row * 128;
-              const int u0 = 2 * (q & 3), odd = q >> 2;
-              const uint4 ev = make_uint4(o[0], o[1], o[2], o[3]), od = make_uint4(o[4], o[5], o[6], o[7]);
-              *reinterpret_cast<uint4*>(rp + (((u0 + odd) ^ (row & 7)) * 16)) = odd ? od : ev;
-              *reinterpret_cast<uint4*>(rp + (((u0 + 1 - odd) ^ (row & 7)) * 16)) = odd ? ev : od;
-            }
-            }
-#ifdef MLA_TC_TRACE
-            const long long tc1 = clock64();
-            w_conv += tc1 - tc0;
-#endif
-            fence_proxy_async();
-            __syncwarp();
-            const bool staged_done = j % kUnitsPerStage == kUnitsPerStage - 1;
-            if (lane == 0) {
-              if (staged_done) mbar_arrive_local(bar(L::PST_EMPTY + stage.slot));
-              mbar_arrive_cluster(leader_bar(L::PV_FULL + unit.slot));
-            }
-#ifdef MLA_TC_TRACE
-            w_fence += clock64() - tc1;
-#endif
-            if (staged_done) stage.advance(L::PStSlots);
-            unit.advance(L::PVSlots);
-          }
-        }
-        if (!ok) break;
-#ifdef MLA_TC_TRACE
-        if (ct == 0) {
-          TC_TRACE_VAL(12, gt, w_unit);
-          TC_TRACE_VAL(13, gt, w_stage);
-          TC_TRACE_VAL(14, gt, clock64() - t_tile);
-          TC_TRACE_VAL(0, gt, w_conv);
-          TC_TRACE_VAL(5, gt, w_fence);
-        }
-#endif
-        __syncwarp();
-        if (lane == 0) mbar_arrive_local(bar(L::SCL_EMPTY + (gt & 1)));
-      }
-    }
-  } else if (warp == L::QKWarp) {
-    // ----------------------------------------------------------- MMA: S = Q K^T
-    if (rank == 0 && lane == 0) {
-      RingConsumer ring{bar(L::QK_FULL), bar(L::QK_EMPTY), L::QKSlots};
-      SegmentWalker walk(p, w, t);
-      Segment s;
-      uint32_t g = 0, seg = 0;
-      bool ok = true;
-      // descriptors advance by adding (byte offset >> 4) to the start-address field
-      const uint64_t qdesc = sdesc(sbase + L::OffQ, 16, 1024);      // chunk c: + 512 c; K-step: + 2
-      const uint64_t kdesc = sdesc(sbase + L::OffQKRing, 16, 1024);  // slot: + 1024 slot
-      while (ok && walk.next(s)) {
-        if (s.n_pages == 0) continue;
-        const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
-        for (int it = 0; it < n_tiles && ok; ++it, ++g) {
-#ifdef MLA_TC_TRACE
-          const long long tq0 = clock64();
-          long long q_data = 0;
-#endif
-          ok = mbar_wait(bar(L::S_FREE + (g & 1)), ((g >> 1) & 1) ^ 1, abort_flag, p.status);
-#ifdef MLA_TC_TRACE
-          if (!kConv) TC_TRACE_VAL(11, g, clock64() - tq0);
-#endif
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sd = tmem + ((g & 1) ? kColS1 : kColS0);
-          TC_TRACE(7, g);
-#pragma unroll 1
-          for (int c = 0; c < kQKUnits; ++c) {
-            if (it == 0) {  // the segment's queries, chunk c
-              ok = mbar_wait(bar(L::Q_FULL + c), seg & 1, abort_flag, p.status);
-              if (!ok) break;
-            }
-#ifdef MLA_TC_TRACE
-            const long long tw = clock64();
-#endif
-            ok = ring.wait_full(abort_flag, p.status);
-#ifdef MLA_TC_TRACE
-            q_data += clock64() - tw;
-#endif
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t a = qdesc + 512 * c, bb = kdesc + 1024 * ring.pos.slot;
-#pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4)  // 16 columns = 32 bytes into the swizzled rows
-              tc_mma(sd, a + 2 * k4, bb + 2 * k4, kIdescQK, (c | k4) ? 1u : 0u);
-            ring.release();
-          }
-          if (!ok) break;
-          tc_commit_pair(bar(L::S_FULL + (g & 1)));
-          TC_TRACE(1, g);
-#ifdef MLA_TC_TRACE
-          if (!kConv) TC_TRACE_VAL(8, g, q_data);
-#endif
-          if (g == 0) MLA_STAMP_ANY(4);
-          if (it == n_tiles - 1) tc_commit_pair(bar(L::Q_EMPTY));
-        }
-        ++seg;
-      }
-      // completes, in both CTAs, once every MMA this thread issued has finished
-      tc_commit_pair(bar(L::DRAIN));
-    }
-  } else if (warp == L::PVWarp) {
-    // ---------------------------------------------------------- MMA: O += P C
-    if (rank == 0 && lane == 0) {
-      RingConsumer ring{bar(L::PV_FULL), bar(L::PV_EMPTY), L::PVSlots};
-      SegmentWalker walk(p, w, t);
-      Segment s;
-      uint32_t g = 0, seg = 0;
-      bool ok = true;
-      const uint64_t vdesc = sdesc(sbase + L::OffPVRing, 8192, 1024);  // slot: + 1024 slot; K-step: + 128
-      const uint64_t pdesc = sdesc(sbase + L::OffP, 16, 1024);         // page sub-tile: + 512 i; K-step: + 2
-      while (ok && walk.next(s)) {
-        if (s.n_pages == 0) continue;
-        const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
-        for (int it = 0; it < n_tiles && ok; ++it, ++g) {
-#ifdef MLA_TC_TRACE
-          const long long tp0 = clock64();
-          long long v_data = 0;
-#endif
-          ok = mbar_wait(bar(L::P_FULL), g & 1, abort_flag, p.status);
-#ifdef MLA_TC_TRACE
-          if (!kConv) TC_TRACE_VAL(10, g, clock64() - tp0);
-#endif
-          if (!ok) break;
-          if (it == 0 && seg > 0) {  // O of the previous segment must be read out first
-            ok = mbar_wait(bar(L::O_FREE), (seg - 1) & 1, abort_flag, p.status);
-            if (!ok) break;
-          }
-          tc_fence_after();
-          TC_TRACE(2, g);
-#pragma unroll 1
-          for (int i = 0; i < kTilePages && ok; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-#ifdef MLA_TC_TRACE
-              const long long tw = clock64();
-#endif
-              ok = ring.wait_full(abort_flag, p.status);
-#ifdef MLA_TC_TRACE
-              v_data += clock64() - tw;
-#endif
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                tc_mma(tmem + (j ? kColO1 : kColO0), pdesc + 512 * i + 2 * ks,
-                       vdesc + 1024 * ring.pos.slot + 128 * ks, kIdescPV, (it == 0 && i == 0 && ks == 0) ? 0u : 1u);
-              ring.release();
-            }
-          if (!ok) break;
-          tc_commit_pair(bar(L::O_DONE));
-          TC_TRACE(3, g);
-#ifdef MLA_TC_TRACE
-          if (!kConv) TC_TRACE_VAL(9, g, v_data);
-#endif
-          if (g == 0) MLA_STAMP_ANY(6);
-        }
-        ++seg;
-      }
-      tc_commit_pair(bar(L::DRAIN));
-    }
-  } else if (warp < 4) {
+  // Roles by warpgroup.  The 4-bit variant's 512 threads are launched with 128
+  // registers each and share them out anew, so that the softmax holds a tile's
+  // probabilities as the bf16 variant does: 128 x 192 (softmax) + 128 x 64
+  // (issuers, producers) + 256 x 120 (converters) = 63,488 of 65,536.
+  if (warp < 4) {
+    if constexpr (kFp4) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ------------------------------------------------------- softmax, epilogue
     // Thread L (TMEM lane) holds head hl of this CTA; lanes 0-63 see the
     // keys of the leader's pages (0 and 2 of a tile), lanes 64-127 those of the
@@ -1424,7 +837,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
           }
           return true;
         };
-        if constexpr (!kConv) {
+        if constexpr (!kConv || kFp4) {
           // the probabilities are formed while the previous PV runs; only
           // their stores into P wait for it
           uint32_t pk_lo[32], pk_hi[32];
@@ -1526,6 +939,666 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(leader_bar(L::O_FREE));
+    }
+  } else if (kConv && warp >= L::QKConvWarp) {
+    if constexpr (kFp4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+      // ------------------------------------ 4-bit: conversion of both rings' units
+      // One rolled loop serves the QK and the PV converters (measured: with the
+      // loops apart and unrolled, a third of all warp stalls were instruction
+      // fetches).  A staging slot feeds two units; thread ct takes 32 columns
+      // (two blocks) of row ct / 2 in each of a unit's two 8 KB halves: the two
+      // pages of a QK unit, the two 64-column atoms of a PV unit.
+      const bool pv = warp >= L::PVConvWarp;
+      constexpr int kHalves = 8 / L::ConvWarps;  // halves of a unit per thread
+      const int ct = (warp - (pv ? L::PVConvWarp : L::QKConvWarp)) * 32 + lane;
+      const int row = (ct >> 1) & 63, q = ct & 1, a0 = ct >> 7;
+      const uint32_t u0 = (uint32_t)(4 * q) ^ (row & 7);
+      const uint32_t st_full = bar(pv ? L::PST_FULL : L::QST_FULL), st_empty = bar(pv ? L::PST_EMPTY : L::QST_EMPTY);
+      const uint32_t un_empty = bar(pv ? L::PV_EMPTY : L::QK_EMPTY);
+      const uint32_t un_full = leader_bar(pv ? L::PV_FULL : L::QK_FULL);
+      const int st_slots = pv ? L::PStSlots : L::QStSlots;
+      constexpr int un_slots = L::QKSlots;
+      static_assert(L::QKSlots == L::PVSlots, "one ring depth");
+      uint8_t* const ring = smem + (pv ? L::OffPVRing : L::OffQKRing) + row * 128;
+      const uint8_t* const st_base = smem + (pv ? L::OffPSt : L::OffQSt);
+      const uint32_t st_bytes = pv ? L::PStBytes : kStageBytes;
+      // byte strides of the unit (u) and the half (a) in the staged codes and the scales
+      const uint32_t code_u = pv ? 4096 : 32, code_a = pv ? 32 : 4096;
+      const uint32_t scl_u = pv ? 16 : 4, scl_a = pv ? 4 : L::PageScl, ts_a = pv ? 0 : L::PageScl;
+      RingPos unit, stage;
+      uint32_t gt = 0;
+      SegmentWalker walk(p, w, t);
+      Segment s;
+      bool ok = true;
+      while (ok && walk.next(s)) {
+        if (s.n_pages == 0) continue;
+        const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
+        for (int it = 0; it < n_tiles && ok; ++it, ++gt) {
+          const uint8_t* const scl_t = smem + L::OffScl + (gt & 1) * L::SclBytes;
+          if (!pv) {
+            ok = mbar_wait(bar(L::SCL_FULL + (gt & 1)), (gt >> 1) & 1, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+            if (!ok) break;
+          }
+          const int pg0 = s.page_lo + it * kTilePages;
+          const int npg = min(kTilePages, s.n_pages - it * kTilePages);
+#pragma unroll 1
+          for (int c = 0; c < 4 && ok; ++c) {
+            // QK: columns [128 c, 128 c + 128) of this CTA's two pages.  PV: key
+            // position c (page tile_page(c)); rows past its visible keys are zero
+            const int tp = tile_page(c);
+            const bool live = !pv || (tp < npg && row < s.nvis - (pg0 + tp) * kPage);
+            ok = mbar_wait(st_full + 8 * stage.slot, stage.phase, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+            if (!ok) break;
+            const uint8_t* const src = st_base + stage.slot * st_bytes + row * 64 + q * 16;
+            const uint8_t* const scl = pv ? st_base + stage.slot * st_bytes + kStageBytes : scl_t;
+            const uint8_t* const sclr = scl + row * 32 + 2 * q + (pv ? 8 * (int)rank : 8 * c);
+            const uint8_t* const tsr = scl + 2048 + row * 4;
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+              uint4 v[kHalves];
+              uint32_t sc[kHalves];
+              float ts[kHalves];
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) {
+                const int a = kHalves == 2 ? h : a0;
+                v[h] = *reinterpret_cast<const uint4*>(src + u * code_u + a * code_a);
+                sc[h] = *reinterpret_cast<const uint16_t*>(sclr + u * scl_u + a * scl_a);
+                ts[h] = *reinterpret_cast<const float*>(tsr + a * ts_a);
+              }
+              ok = mbar_wait(un_empty + 8 * unit.slot, unit.phase ^ 1, abort_flag, p.status);
+              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+              if (!ok) break;
+              uint8_t* const dst = ring + unit.slot * kUnitBytes;
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) {
+                const int a = kHalves == 2 ? h : a0;
+                __half2 s0, s1;
+                fp4_block_scales(sc[h], __float2half2_rn(ts[h]), s0, s1);
+                if (!live) s0 = s1 = __float2half2_rn(0.f);
+                store_e2m1x32(dst + a * 8192, u0, v[h], s0, s1);
+              }
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(un_full + 8 * unit.slot);
+              unit.advance(un_slots);
+            }
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_local(st_empty + 8 * stage.slot);
+            stage.advance(st_slots);
+          }
+          if (!ok) break;
+          if (!pv) {
+            // k^R: one staged page (64 rows x 64 bf16) per half of the unit
+            ok = mbar_wait(un_empty + 8 * unit.slot, unit.phase ^ 1, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+            if (!ok) break;
+#pragma unroll 1
+            for (int a = 0; a < 2 && ok; ++a) {
+              ok = mbar_wait(st_full + 8 * stage.slot, stage.phase, abort_flag, p.status);
+              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+              if (!ok) break;
+              const uint8_t* const src = st_base + stage.slot * st_bytes;
+              uint8_t* const dst = smem + L::OffQKRing + unit.slot * kUnitBytes + a * 8192;
+#pragma unroll
+              for (int k = 0; k < 2 * kHalves; ++k) {
+                const int r = (ct >> 3) + kConvThreads / 8 * k, u = ct & 7;
+                const uint4 x = *reinterpret_cast<const uint4*>(src + r * 128 + u * 16);
+                *reinterpret_cast<uint4*>(dst + r * 128 + ((u ^ (r & 7)) * 16)) =
+                    make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive_local(st_empty + 8 * stage.slot);
+              stage.advance(st_slots);
+            }
+            if (!ok) break;
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_cluster(un_full + 8 * unit.slot);
+              mbar_arrive_local(bar(L::SCL_EMPTY + (gt & 1)));
+            }
+            unit.advance(un_slots);
+          }
+        }
+      }
+    } else if (warp < L::PVConvWarp) {
+      // ------------------------------------------------- FP8: QK unit conversion
+      // Thread ct of the converter warps converts 16-byte groups ct,
+      // ct + kConvThreads, ... of the staged data into the unit (128-byte swizzle).
+      const int ct = (warp - L::QKConvWarp) * 32 + lane;
+      RingPos unit, stage;
+      uint32_t gt = 0;
+      const int y_pages = 2 * (int)rank;
+      SegmentWalker walk(p, w, t);
+      Segment s;
+      bool ok = true;
+      while (ok && walk.next(s)) {
+        if (s.n_pages == 0) continue;
+        const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
+        for (int it = 0; it < n_tiles && ok; ++it, ++gt) {
+          ok = mbar_wait(bar(L::SCL_FULL + (gt & 1)), (gt >> 1) & 1, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+          if (!ok) break;
+          // the tile's scales, [4 pages][64 rows][4 tiles of 128 columns]
+          const float* scl = reinterpret_cast<const float*>(smem + L::OffScl + (gt & 1) * L::SclBytes);
+#ifdef MLA_TC_TRACE
+          long long w_unit = 0, w_stage = 0, t_tile = clock64();
+#endif
+          for (int c = 0; c < kQKUnits && ok; ++c) {
+#ifdef MLA_TC_TRACE
+            long long tw = clock64();
+#endif
+            ok = mbar_wait(bar(L::QK_EMPTY + unit.slot), unit.phase ^ 1, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+#ifdef MLA_TC_TRACE
+            w_unit += clock64() - tw;
+            tw = clock64();
+#endif
+            if (!ok) break;
+            uint8_t* dstu = smem + L::OffQKRing + unit.slot * kUnitBytes;
+            if (c < kChunks - 1) {
+              // [2 pages][64 rows][64 codes]; the scale of columns [64c, 64c+64) is tile c/2
+              ok = mbar_wait(bar(L::QST_FULL + stage.slot), stage.phase, abort_flag, p.status);
+              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+#ifdef MLA_TC_TRACE
+              w_stage += clock64() - tw;
+#endif
+              if (!ok) break;
+              const uint8_t* src = smem + L::OffQSt + stage.slot * kStageBytes;
+              constexpr int kG = 512 / kConvThreads;  // 16-byte groups per thread
+              // all of the thread's codes and scales are loaded before any store
+              uint4 v[kG];
+              float sc[kG];
+#pragma unroll
+              for (int k = 0; k < kG; ++k) {
+                const int gi = k * kConvThreads + ct, r = gi >> 2, q = gi & 3;  // r: unit row (this CTA's page r/64)
+                v[k] = *reinterpret_cast<const uint4*>(src + r * 64 + q * 16);
+                sc[k] = scl[(tile_page(y_pages + (r >> 6)) * 64 + (r & 63)) * 4 + (c >> 1)];
+              }
+#pragma unroll
+              for (int k = 0; k < kG; ++k) {
+                const int gi = k * kConvThreads + ct, r = gi >> 2, q = gi & 3;
+                const __half2 s2 = __float2half2_rn(sc[k]);
+                uint32_t o[8];
+                e4m3x4_scaled(v[k].x, s2, o[0], o[1]);
+                e4m3x4_scaled(v[k].y, s2, o[2], o[3]);
+                e4m3x4_scaled(v[k].z, s2, o[4], o[5]);
+                e4m3x4_scaled(v[k].w, s2, o[6], o[7]);
+                uint8_t* rp = dstu + r * 128;
+                *reinterpret_cast<uint4*>(rp + (((2 * q) ^ (r & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(rp + (((2 * q + 1) ^ (r & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+              }
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_local(bar(L::QST_EMPTY + stage.slot));
+              stage.advance(L::QStSlots);
+            } else {
+              // k^R: one staged page (64 rows x 64 bf16) per half of the unit
+              for (int i = 0; i < 2 && ok; ++i) {
+                ok = mbar_wait(bar(L::QST_FULL + stage.slot), stage.phase, abort_flag, p.status);
+                ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+                if (!ok) break;
+                const uint8_t* src = smem + L::OffQSt + stage.slot * kStageBytes;
+                uint8_t* dst = dstu + i * 8192;
+                constexpr int kG = 512 / kConvThreads;
+                uint4 v[kG];
+#pragma unroll
+                for (int k = 0; k < kG; ++k) {
+                  const int gi = k * kConvThreads + ct, row = gi >> 3, u = gi & 7;
+                  v[k] = *reinterpret_cast<const uint4*>(src + row * 128 + u * 16);
+                }
+#pragma unroll
+                for (int k = 0; k < kG; ++k) {
+                  const int gi = k * kConvThreads + ct, row = gi >> 3, u = gi & 7;
+                  *reinterpret_cast<uint4*>(dst + row * 128 + ((u ^ (row & 7)) * 16)) =
+                      make_uint4(bf16x2_to_f16x2(v[k].x), bf16x2_to_f16x2(v[k].y), bf16x2_to_f16x2(v[k].z),
+                                 bf16x2_to_f16x2(v[k].w));
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_local(bar(L::QST_EMPTY + stage.slot));
+                stage.advance(L::QStSlots);
+              }
+              if (!ok) break;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(leader_bar(L::QK_FULL + unit.slot));
+            unit.advance(L::QKSlots);
+          }
+          if (!ok) break;
+#ifdef MLA_TC_TRACE
+          if (ct == 0) {
+            TC_TRACE_VAL(8, gt, w_unit);
+            TC_TRACE_VAL(9, gt, w_stage);
+            TC_TRACE_VAL(10, gt, clock64() - t_tile);
+            TC_TRACE(11, gt);
+          }
+#endif
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(bar(L::SCL_EMPTY + (gt & 1)));
+        }
+      }
+    } else {
+      // ------------------------------------------------- FP8: PV unit conversion
+      const int ct = (warp - L::PVConvWarp) * 32 + lane;
+      const int blk = (int)rank;  // + 2j: this CTA's 128 columns of half j are scale tile 2j + rank
+      RingPos unit, stage;
+      uint32_t gt = 0;
+      SegmentWalker walk(p, w, t);
+      Segment s;
+      bool ok = true;
+      while (ok && walk.next(s)) {
+        if (s.n_pages == 0) continue;
+        const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
+        for (int it = 0; it < n_tiles && ok; ++it, ++gt) {
+          ok = mbar_wait(bar(L::SCL_FULL + (gt & 1)), (gt >> 1) & 1, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+          if (!ok) break;
+          const float* scl_t = reinterpret_cast<const float*>(smem + L::OffScl + (gt & 1) * L::SclBytes);
+          const int pg0 = s.page_lo + it * kTilePages;
+          const int npg = min(kTilePages, s.n_pages - it * kTilePages);
+#ifdef MLA_TC_TRACE
+          long long w_unit = 0, w_stage = 0, w_conv = 0, w_fence = 0, t_tile = clock64();
+#endif
+          for (int i = 0; i < kTilePages && ok; ++i) {
+            const int tp = tile_page(i);
+            const int valid = tp < npg ? min(kPage, s.nvis - (pg0 + tp) * kPage) : 0;
+            const float* scl = scl_t + tp * 256;
+            for (int j = 0; j < 2 && ok; ++j) {
+#ifdef MLA_TC_TRACE
+              long long tw = clock64();
+#endif
+              ok = mbar_wait(bar(L::PV_EMPTY + unit.slot), unit.phase ^ 1, abort_flag, p.status);
+              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+              if (!ok) break;
+#ifdef MLA_TC_TRACE
+              w_unit += clock64() - tw;
+              tw = clock64();
+#endif
+              ok = mbar_wait(bar(L::PST_FULL + stage.slot), stage.phase, abort_flag, p.status);
+              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
+              if (!ok) break;
+#ifdef MLA_TC_TRACE
+              w_stage += clock64() - tw;
+#endif
+              const uint8_t* src = smem + L::OffPSt + stage.slot * L::PStBytes;
+              uint8_t* dst = smem + L::OffPVRing + unit.slot * kUnitBytes;
+#ifdef MLA_TC_TRACE
+              const long long tc0 = clock64();
+#endif
+              // 64 rows x 128 codes -> two 64-column atoms (8 KB apart); rows
+              // past the visible keys are zero
+              constexpr int kG = 512 / kConvThreads;
+              // all of the thread's codes and scales are loaded before any store
+              uint4 v[kG];
+              float sc[kG];
+#pragma unroll
+              for (int k = 0; k < kG; ++k) {
+                const int gi = k * kConvThreads + ct, row = gi >> 3, q = gi & 7;
+                v[k] = make_uint4(0, 0, 0, 0);
+                sc[k] = 0.f;
+                if (row < valid) {
+                  v[k] = *reinterpret_cast<const uint4*>(src + row * 128 + q * 16);
+                  sc[k] = scl[row * 4 + 2 * j + blk];
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < kG; ++k) {
+                const int gi = k * kConvThreads + ct, row = gi >> 3, q = gi & 7;
+                uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (row < valid) {
+                  const __half2 s2 = __float2half2_rn(sc[k]);
+                  e4m3x4_scaled(v[k].x, s2, o[0], o[1]);
+                  e4m3x4_scaled(v[k].y, s2, o[2], o[3]);
+                  e4m3x4_scaled(v[k].z, s2, o[4], o[5]);
+                  e4m3x4_scaled(v[k].w, s2, o[6], o[7]);
+                }
+                // the eight threads of a row cover both 64-column atoms; threads
+                // of the second atom store their odd unit first, so the two
+                // stores of each phase fall on distinct banks
+                uint8_t* rp = dst + (q >> 2) * 8192 + row * 128;
+                const int u0 = 2 * (q & 3), odd = q >> 2;
+                const uint4 ev = make_uint4(o[0], o[1], o[2], o[3]), od = make_uint4(o[4], o[5], o[6], o[7]);
+                *reinterpret_cast<uint4*>(rp + (((u0 + odd) ^ (row & 7)) * 16)) = odd ? od : ev;
+                *reinterpret_cast<uint4*>(rp + (((u0 + 1 - odd) ^ (row & 7)) * 16)) = odd ? ev : od;
+              }
+#ifdef MLA_TC_TRACE
+              const long long tc1 = clock64();
+              w_conv += tc1 - tc0;
+#endif
+              fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive_local(bar(L::PST_EMPTY + stage.slot));
+                mbar_arrive_cluster(leader_bar(L::PV_FULL + unit.slot));
+              }
+#ifdef MLA_TC_TRACE
+              w_fence += clock64() - tc1;
+#endif
+              stage.advance(L::PStSlots);
+              unit.advance(L::PVSlots);
+            }
+          }
+          if (!ok) break;
+#ifdef MLA_TC_TRACE
+          if (ct == 0) {
+            TC_TRACE_VAL(12, gt, w_unit);
+            TC_TRACE_VAL(13, gt, w_stage);
+            TC_TRACE_VAL(14, gt, clock64() - t_tile);
+            TC_TRACE_VAL(0, gt, w_conv);
+            TC_TRACE_VAL(5, gt, w_fence);
+          }
+#endif
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(bar(L::SCL_EMPTY + (gt & 1)));
+        }
+      }
+    }
+  } else {
+    if constexpr (kFp4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp >= L::QKProdWarp && warp < L::QKProdWarp + L::Producers) {
+      // -------------------------------------------------------------- TMA: Q, QK
+      if (lane == 0 && !stall) {
+        const int pid = warp - L::QKProdWarp;
+        RingProducer ring{kConv ? L::QStSlots : L::QKSlots, L::Producers, pid};
+        const uint32_t empty0 = kConv ? bar(L::QST_EMPTY) : bar(L::QK_EMPTY);
+        const int y_pages = 2 * (int)rank;  // this CTA's key positions of a tile (pages tile_page(...))
+        SegmentWalker walk(p, w, t);
+        Segment s;
+        uint32_t seg = 0, gtile = 0;
+        bool ok = true;
+        while (ok && walk.next(s)) {
+          if (s.n_pages == 0) continue;
+          // absorbed queries of this CTA's 64 heads for (b, t)
+          if (pid == 0) {
+            if (seg > 0) ok = mbar_wait(bar(L::Q_EMPTY), (seg - 1) & 1, abort_flag, p.status);
+            if (!ok) break;
+            // one barrier per 64-column chunk: the first tile's MMAs of unit c
+            // wait only for chunk c
+            if (rank == 0)
+              for (int c = 0; c < kChunks; ++c) mbar_expect_tx(bar(L::Q_FULL + c), 2 * 8192);
+            const int qrow = ((s.b * p.n_q + t) * kHeads) + kHalfHeads * (int)rank;
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_2d_pair(sbase + L::OffQ + c * 8192, &P.map_q, 64 * c, qrow, leader_bar(L::Q_FULL + c));
+          }
+          const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
+          for (int it = 0; it < n_tiles && ok; ++it) {
+            const int pg0 = s.page_lo + it * kTilePages;
+            const int npg = min(kTilePages, s.n_pages - it * kTilePages);
+            // this CTA's pages; pages past the tile's end come from outside the
+            // tensor (zero fill)
+            int pg[2];
+            for (int i = 0; i < 2; ++i) {
+              const int tp = tile_page(y_pages + i);
+              pg[i] = tp < npg ? page_of(s.b, pg0 + tp) : -1;
+            }
+            if constexpr (kConv) {
+              // this CTA's pages two tiles ahead (at a segment's start also one
+              // ahead) go to L2 now, so that the staging loads find them there.
+              // (Measured: a gain for the FP8 cache, whose converters bound the
+              // tile; a loss for bf16, whose ring loads wait behind the bulk
+              // prefetches in the TMA unit.)  Invalid entries are skipped here
+              // and reported when their tile is loaded.
+              if (pid == 0) {
+                for (int d = it == 0 ? 1 : 2; d <= 2 && it + d < n_tiles; ++d) {
+                  const int pgp = s.page_lo + (it + d) * kTilePages;
+                  const int npgp = min(kTilePages, s.n_pages - (it + d) * kTilePages);
+                  for (int i = 0; i < 2; ++i) {
+                    const int tp = tile_page(y_pages + i);
+                    if (tp >= npgp) continue;
+                    const int page = p.page_table[(size_t)s.b * p.max_pages + pgp + tp];
+                    if (page >= 0 && page < p.num_pages)
+                      prefetch_l2(p.pool + (size_t)page * p.page_bytes, (uint32_t)p.page_bytes);
+                  }
+                }
+              }
+              // scales of the tile's four pages (zero for pages past its end)
+              if (pid == 0) {
+                const uint32_t sb = gtile & 1;
+                ok = mbar_wait(bar(L::SCL_EMPTY + sb), ((gtile >> 1) & 1) ^ 1, abort_flag, p.status);
+                if (!ok) break;
+                const uint32_t fb = bar(L::SCL_FULL + sb);
+                mbar_arrive_tx_local(fb, L::SclBytes);
+                for (int i = 0; i < L::SclPages; ++i) {
+                  const uint32_t dst = sbase + L::OffScl + sb * L::SclBytes + i * L::PageScl;
+                  if constexpr (kFp4)  // (a page past the tile's end: the first page's scales; its scores are masked)
+                    bulk_load(dst, p.pool + (size_t)(pg[i] >= 0 ? pg[i] : page_of(s.b, pg0)) * p.page_bytes + P.scl_off,
+                              L::PageScl, fb);
+                  else
+                    tma_load_3d(dst, &P.map_scl, 0, 0, i < npg ? page_of(s.b, pg0 + i) : -1, fb);
+                }
+              }
+              ++gtile;
+            }
+            for (int c = 0; c < kQKUnits; ++c) {
+              if constexpr (!kConv) {
+                uint32_t slot;
+                if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
+                if (rank == 0) mbar_expect_tx(bar(L::QK_FULL + slot), 2 * kUnitBytes);
+                const uint32_t dst = sbase + L::OffQKRing + slot * kUnitBytes, fb = leader_bar(L::QK_FULL + slot);
+                for (int i = 0; i < 2; ++i)
+                  tma_load_2d_pair(dst + i * 8192, &P.map_pv, 64 * c, pg[i] >= 0 ? pg[i] * kPage : -kPage, fb);
+              } else if (c < kChunks - 1) {
+                // codes of columns [64c, 64c+64) of both pages (4-bit: of 128
+                // columns, for two units): one staging slot
+                if (c % kUnitsPerStage != 0) continue;
+                uint32_t slot;
+                if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
+                const uint32_t dst = sbase + L::OffQSt + slot * kStageBytes, fb = bar(L::QST_FULL + slot);
+                mbar_arrive_tx_local(fb, kStageBytes);
+                for (int i = 0; i < 2; ++i)
+                  tma_load_3d(dst + i * 4096, &P.map_codes_qk, kFp4 ? 32 * c : 64 * c, 0, pg[i], fb);
+              } else {
+                // k^R: one staging slot per page
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t slot;
+                  if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
+                  const uint32_t dst = sbase + L::OffQSt + slot * kStageBytes, fb = bar(L::QST_FULL + slot);
+                  mbar_arrive_tx_local(fb, kStageBytes);
+                  tma_load_3d(dst, &P.map_kr, 0, 0, pg[i], fb);
+                }
+              }
+            }
+          }
+          ++seg;
+        }
+      }
+    } else if (warp >= L::PVProdWarp) {
+      // ------------------------------------------------------------------ TMA: PV
+      if (lane == 0 && !stall) {
+        RingProducer ring{kConv ? L::PStSlots : L::PVSlots, L::Producers, warp - L::PVProdWarp};
+        const uint32_t empty0 = kConv ? bar(L::PST_EMPTY) : bar(L::PV_EMPTY);
+        const int x_pv = 128 * (int)rank;  // this CTA's 128 columns of an N=256 half
+        SegmentWalker walk(p, w, t);
+        Segment s;
+        bool ok = true;
+        while (ok && walk.next(s)) {
+          if (s.n_pages == 0) continue;
+          const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
+          for (int it = 0; it < n_tiles && ok; ++it) {
+            const int pg0 = s.page_lo + it * kTilePages;
+            const int npg = min(kTilePages, s.n_pages - it * kTilePages);
+            // key position i outer (page tile_page(i)), N-half j inner
+            for (int i = 0; i < kTilePages; ++i) {
+              const int tp = tile_page(i);
+              const int valid = tp < npg ? min(kPage, s.nvis - (pg0 + tp) * kPage) : 0;
+              const int page = valid > 0 ? page_of(s.b, pg0 + tp) : 0;
+              for (int j = 0; j < 2; ++j) {
+                if (kFp4 && j == 1) break;  // one slot holds both halves' codes
+                uint32_t slot;
+                if (!ring.claim(empty0, slot, ok, abort_flag, p.status)) continue;
+                const int x0 = 256 * j + x_pv;
+                if constexpr (kFp4) {
+                  const uint32_t fb = bar(L::PST_FULL + slot);
+                  const uint32_t dst = sbase + L::OffPSt + slot * L::PStBytes;
+                  mbar_arrive_tx_local(fb, valid > 0 ? L::PStBytes : kStageBytes);
+                  for (int jj = 0; jj < 2; ++jj)
+                    tma_load_3d(dst + jj * 4096, &P.map_codes_pv, (256 * jj + x_pv) / 2, 0, valid > 0 ? page : -1, fb);
+                  if (valid > 0)  // (no key of the page visible: the converters read no scale)
+                    bulk_load(dst + kStageBytes, p.pool + (size_t)page * p.page_bytes + P.scl_off, L::PageScl, fb);
+                } else if constexpr (kConv) {
+                  // the converters zero the rows past the visible keys
+                  const uint32_t fb = bar(L::PST_FULL + slot);
+                  mbar_arrive_tx_local(fb, kStageBytes);
+                  tma_load_3d(sbase + L::OffPSt + slot * kStageBytes, &P.map_codes_pv, x0, 0, valid > 0 ? page : -1, fb);
+                } else {
+                  // Rows past the visible keys and pages past the tile's end
+                  // come from outside the tensor (zero fill), so 0 * (whatever
+                  // the pool held) cannot reach O.
+                  if (rank == 0) mbar_expect_tx(bar(L::PV_FULL + slot), 2 * kUnitBytes);
+                  const uint32_t dst = sbase + L::OffPVRing + slot * kUnitBytes, fb = leader_bar(L::PV_FULL + slot);
+                  for (int a = 0; a < 2; ++a) {
+                    const int x = x0 + 64 * a;
+                    const uint32_t d = dst + a * 8192;
+                    if (valid == kPage) {
+                      tma_load_2d_pair(d, &P.map_pv, x, page * kPage, fb);
+                    } else if (valid <= 0) {
+                      tma_load_2d_pair(d, &P.map_pv, x, -kPage, fb);
+                    } else {
+                      for (int q = 0; q < 4; ++q) {
+                        if (16 * q + 16 <= valid) {
+                          tma_load_2d_pair(d + q * 2048, &P.map_pv16, x, page * kPage + 16 * q, fb);
+                        } else if (16 * q >= valid) {
+                          tma_load_2d_pair(d + q * 2048, &P.map_pv16, x, -16, fb);
+                        } else {
+                          for (int k = 0; k < 16; ++k)
+                            tma_load_2d_pair(d + (16 * q + k) * 128, &P.map_row, x,
+                                             16 * q + k < valid ? page * kPage + 16 * q + k : -1, fb);
+                        }
+                      }
+                    }
+                  }
+                }
+              }
+            }
+          }
+        }
+      }
+    } else if (warp == L::QKWarp) {
+      // ----------------------------------------------------------- MMA: S = Q K^T
+      if (rank == 0 && lane == 0) {
+        RingConsumer ring{bar(L::QK_FULL), bar(L::QK_EMPTY), L::QKSlots};
+        SegmentWalker walk(p, w, t);
+        Segment s;
+        uint32_t g = 0, seg = 0;
+        bool ok = true;
+        // descriptors advance by adding (byte offset >> 4) to the start-address field
+        const uint64_t qdesc = sdesc(sbase + L::OffQ, 16, 1024);      // chunk c: + 512 c; K-step: + 2
+        const uint64_t kdesc = sdesc(sbase + L::OffQKRing, 16, 1024);  // slot: + 1024 slot
+        while (ok && walk.next(s)) {
+          if (s.n_pages == 0) continue;
+          const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
+          for (int it = 0; it < n_tiles && ok; ++it, ++g) {
+#ifdef MLA_TC_TRACE
+            const long long tq0 = clock64();
+            long long q_data = 0;
+#endif
+            ok = mbar_wait(bar(L::S_FREE + (g & 1)), ((g >> 1) & 1) ^ 1, abort_flag, p.status);
+#ifdef MLA_TC_TRACE
+            if (!kConv) TC_TRACE_VAL(11, g, clock64() - tq0);
+#endif
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sd = tmem + ((g & 1) ? kColS1 : kColS0);
+            TC_TRACE(7, g);
+#pragma unroll 1
+            for (int c = 0; c < kQKUnits; ++c) {
+              if (it == 0) {  // the segment's queries, chunk c
+                ok = mbar_wait(bar(L::Q_FULL + c), seg & 1, abort_flag, p.status);
+                if (!ok) break;
+              }
+#ifdef MLA_TC_TRACE
+              const long long tw = clock64();
+#endif
+              ok = ring.wait_full(abort_flag, p.status);
+#ifdef MLA_TC_TRACE
+              q_data += clock64() - tw;
+#endif
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t a = qdesc + 512 * c, bb = kdesc + 1024 * ring.pos.slot;
+#pragma unroll
+              for (int k4 = 0; k4 < 4; ++k4)  // 16 columns = 32 bytes into the swizzled rows
+                tc_mma(sd, a + 2 * k4, bb + 2 * k4, kIdescQK, (c | k4) ? 1u : 0u);
+              ring.release();
+            }
+            if (!ok) break;
+            tc_commit_pair(bar(L::S_FULL + (g & 1)));
+            TC_TRACE(1, g);
+#ifdef MLA_TC_TRACE
+            if (!kConv) TC_TRACE_VAL(8, g, q_data);
+#endif
+            if (g == 0) MLA_STAMP_ANY(4);
+            if (it == n_tiles - 1) tc_commit_pair(bar(L::Q_EMPTY));
+          }
+          ++seg;
+        }
+        // completes, in both CTAs, once every MMA this thread issued has finished
+        tc_commit_pair(bar(L::DRAIN));
+      }
+    } else if (warp == L::PVWarp) {
+      // ---------------------------------------------------------- MMA: O += P C
+      if (rank == 0 && lane == 0) {
+        RingConsumer ring{bar(L::PV_FULL), bar(L::PV_EMPTY), L::PVSlots};
+        SegmentWalker walk(p, w, t);
+        Segment s;
+        uint32_t g = 0, seg = 0;
+        bool ok = true;
+        const uint64_t vdesc = sdesc(sbase + L::OffPVRing, 8192, 1024);  // slot: + 1024 slot; K-step: + 128
+        const uint64_t pdesc = sdesc(sbase + L::OffP, 16, 1024);         // page sub-tile: + 512 i; K-step: + 2
+        while (ok && walk.next(s)) {
+          if (s.n_pages == 0) continue;
+          const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
+          for (int it = 0; it < n_tiles && ok; ++it, ++g) {
+#ifdef MLA_TC_TRACE
+            const long long tp0 = clock64();
+            long long v_data = 0;
+#endif
+            ok = mbar_wait(bar(L::P_FULL), g & 1, abort_flag, p.status);
+#ifdef MLA_TC_TRACE
+            if (!kConv) TC_TRACE_VAL(10, g, clock64() - tp0);
+#endif
+            if (!ok) break;
+            if (it == 0 && seg > 0) {  // O of the previous segment must be read out first
+              ok = mbar_wait(bar(L::O_FREE), (seg - 1) & 1, abort_flag, p.status);
+              if (!ok) break;
+            }
+            tc_fence_after();
+            TC_TRACE(2, g);
+#pragma unroll 1
+            for (int i = 0; i < kTilePages && ok; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+#ifdef MLA_TC_TRACE
+                const long long tw = clock64();
+#endif
+                ok = ring.wait_full(abort_flag, p.status);
+#ifdef MLA_TC_TRACE
+                v_data += clock64() - tw;
+#endif
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  tc_mma(tmem + (j ? kColO1 : kColO0), pdesc + 512 * i + 2 * ks,
+                         vdesc + 1024 * ring.pos.slot + 128 * ks, kIdescPV, (it == 0 && i == 0 && ks == 0) ? 0u : 1u);
+                ring.release();
+              }
+            if (!ok) break;
+            tc_commit_pair(bar(L::O_DONE));
+            TC_TRACE(3, g);
+#ifdef MLA_TC_TRACE
+            if (!kConv) TC_TRACE_VAL(9, g, v_data);
+#endif
+            if (g == 0) MLA_STAMP_ANY(6);
+          }
+          ++seg;
+        }
+        tc_commit_pair(bar(L::DRAIN));
+      }
     }
   }
 
