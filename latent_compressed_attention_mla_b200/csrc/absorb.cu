@@ -6,7 +6,8 @@
 // decode kernel scores against the 576-wide cached rows.
 //
 // The output is in the activation type, or f16 when the decode path reads
-// f16 queries (FP8 cache on the tensor cores).
+// f16 queries (FP8 and 4-bit caches on the tensor cores; the rotated q^R stays
+// bf16 for a 4-bit cache).
 //
 // bf16 activations at DeepSeek-V3 dims (absorb_tc_kernel): one CTA per (head,
 // block of 32, 64 or 128 tokens; the largest block that still gives every SM a
@@ -144,7 +145,8 @@ __device__ void build_plan(const AbsorbArgs& a) {
   }
 }
 
-template <typename T, typename TO>
+// TO: type of q~ in q_abs; TR: of the rotated q^R (the same size)
+template <typename T, typename TO, typename TR = TO>
 __global__ void __launch_bounds__(128) absorb_kernel(const AbsorbArgs a) {
   constexpr int VEC = VecN<T>::n;
   __shared__ float q_s[kTokBlock][kDG * kMaxRows];
@@ -228,9 +230,9 @@ __global__ void __launch_bounds__(128) absorb_kernel(const AbsorbArgs a) {
       rope_cos_sin(p, k, half, a.rope_base, &cs, &sn);
       const T* src = qr + ((size_t)m * a.n_heads + h) * a.d_rope;
       const float x1 = to_f(src[k]), x2 = to_f(src[half + k]);
-      TO* dst = qa + ((size_t)m * a.n_heads + h) * D + a.d_c;
-      dst[k] = from_f<TO>(x1 * cs - x2 * sn);
-      dst[half + k] = from_f<TO>(x2 * cs + x1 * sn);
+      TR* dst = reinterpret_cast<TR*>(qa) + ((size_t)m * a.n_heads + h) * D + a.d_c;
+      dst[k] = from_f<TR>(x1 * cs - x2 * sn);
+      dst[half + k] = from_f<TR>(x2 * cs + x1 * sn);
     }
   }
   tl_end(a.timeline, MLA_TRACE_ABSORB);
@@ -377,7 +379,7 @@ __device__ __forceinline__ uint32_t pack2(float x, float y, __half*) {
 // their weights while it runs) warp w owns [128w, 128w + 128) and one 16-row
 // tile at a time.  Each result goes through a swizzled shared-memory stage so
 // that every output row leaves as 1 KB of 16-byte stores.
-template <typename TO, int TOK, int THREADS, int NSPLIT>
+template <typename TO, int TOK, int THREADS, int NSPLIT, typename TR = TO>
 __global__ void __launch_bounds__(THREADS) absorb_tc_kernel(const __grid_constant__ AbsorbTcArgs P) {
   constexpr int kCols = kTcDc / NSPLIT;  // output columns of this CTA
   constexpr int kWarps = THREADS / 32, kColsW = kCols / kWarps, kNP = kColsW / 16;
@@ -428,9 +430,9 @@ __global__ void __launch_bounds__(THREADS) absorb_tc_kernel(const __grid_constan
   // and query rows land (in the first column part's CTA)
   if (part == 0) {
     if (a.d_rope == 64 && P.rope_v8 && mc >= 8)
-      rope_query_rows_v8<TO, (TOK * 4 + THREADS - 1) / THREADS>(a, h, m0, mc);
+      rope_query_rows_v8<TR, (TOK * 4 + THREADS - 1) / THREADS>(a, h, m0, mc);
     else
-      rope_query_rows<__nv_bfloat16, TO>(a, h, m0, mc);
+      rope_query_rows<__nv_bfloat16, TR>(a, h, m0, mc);
   }
   MLA_STAMP(4);
   cp_async_wait<0>();
@@ -497,7 +499,7 @@ bool absorb_tc_fits(const mla_dims& d) { return d.d_nope == kTcDn && d.d_c == kT
 
 cudaError_t launch_absorb_and_plan(const mla_dims& d, const void* q_nope, const void* q_rope, const void* W_uk,
                                    const int32_t* seq_lens, int batch, int n_q, int max_pages, int splits,
-                                   void* q_abs, bool q_abs_f16, int32_t* plan, float* lse_part, size_t lse_count,
+                                   void* q_abs, bool q_abs_f16, bool q_rope_bf16, int32_t* plan, float* lse_part, size_t lse_count,
                                    int* status, cudaStream_t st) {
   AbsorbArgs a;
   a.q_nope = q_nope;
@@ -546,7 +548,12 @@ cudaError_t launch_absorb_and_plan(const mla_dims& d, const void* q_nope, const 
     auto pick = [&](auto k32n, auto k32, auto k64, auto k128) {
       return tok == 128 ? k128 : tok == 64 ? k64 : narrow ? k32n : k32;
     };
-    auto kernel = q_abs_f16 ? pick(absorb_tc_kernel<__half, 32, 128, 2>, absorb_tc_kernel<__half, 32, 256, 1>,
+    auto kernel = q_rope_bf16
+                      ? pick(absorb_tc_kernel<__half, 32, 128, 2, __nv_bfloat16>,
+                             absorb_tc_kernel<__half, 32, 256, 1, __nv_bfloat16>,
+                             absorb_tc_kernel<__half, 64, 256, 1, __nv_bfloat16>,
+                             absorb_tc_kernel<__half, 128, 256, 1, __nv_bfloat16>)
+                  : q_abs_f16 ? pick(absorb_tc_kernel<__half, 32, 128, 2>, absorb_tc_kernel<__half, 32, 256, 1>,
                                    absorb_tc_kernel<__half, 64, 256, 1>, absorb_tc_kernel<__half, 128, 256, 1>)
                             : pick(absorb_tc_kernel<__nv_bfloat16, 32, 128, 2>,
                                    absorb_tc_kernel<__nv_bfloat16, 32, 256, 1>,
@@ -561,6 +568,8 @@ cudaError_t launch_absorb_and_plan(const mla_dims& d, const void* q_nope, const 
   const dim3 grid(d.n_heads, (d.d_c + kCG * vec - 1) / (kCG * vec));
   if (d.act_dtype == MLA_F32)
     absorb_kernel<float, float><<<grid, 128, 0, st>>>(a);
+  else if (q_rope_bf16)
+    absorb_kernel<__nv_bfloat16, __half, __nv_bfloat16><<<grid, 128, 0, st>>>(a);
   else if (q_abs_f16)
     absorb_kernel<__nv_bfloat16, __half><<<grid, 128, 0, st>>>(a);
   else

@@ -45,7 +45,9 @@
 //  * 4-bit cache: the FP8 scheme with other converters: e2m1 pairs become f16
 //    by one conversion and one multiply with the block's scale times the token's
 //    (at most six significant bits, so exact wherever f16 holds the value's
-//    range).  A staging slot holds 128 columns, enough for two units.
+//    range).  A staging slot holds 128 columns, enough for two units.  k^R and
+//    q^R stay bf16: TMA brings the k^R unit straight into the ring, and its
+//    MMAs take the bf16 form.
 //  * Warp roles: 0-3 softmax + epilogue (one TMEM lane each), 4 TMEM
 //    allocation and (leader) QK issue, 5 (leader) PV issue; bf16 cache: 6-7
 //    TMA for Q and QK data, 8-9 TMA for PV data; FP8 cache: 6 / 7 TMA for
@@ -100,7 +102,8 @@ struct TcLayout {
   // brings its page's scales along.
   static constexpr int SclBufs = kConv ? 2 : 0, SclPages = kFp4 ? 2 : kTilePages;
   static constexpr uint32_t PageScl = kPageScl<kCache>, SclBytes = SclPages * PageScl;
-  static constexpr uint32_t PStBytes = kStageBytes + (kFp4 ? PageScl : 0);
+  // (4-bit slots are 512-byte aligned: their codes carry the 64-byte swizzle)
+  static constexpr uint32_t PStBytes = kStageBytes + (kFp4 ? (PageScl + 511) / 512 * 512 : 0);
   static constexpr uint32_t OffQ = 0;
   static constexpr uint32_t OffP = OffQ + kQBytes;
   static constexpr uint32_t OffQKRing = OffP + kPBytes;
@@ -375,6 +378,15 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t 
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                                 uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -550,7 +562,7 @@ struct TcParams {
   // FP8 and 4-bit caches: [pages][64 rows][...] views of the page sub-blocks
   CUtensorMap map_codes_qk;  // FP8: box 64 codes x 64 rows (one page's part of a QK unit); 4-bit: map_codes_pv's
   CUtensorMap map_codes_pv;  // box 128 codes (128 or 64 bytes) x 64 rows (one PV unit)
-  CUtensorMap map_kr;        // bf16 k^R, box 64 x 64 rows
+  CUtensorMap map_kr;        // bf16 k^R, box 64 x 64 rows (4-bit: 128-byte swizzle)
   CUtensorMap map_scl;       // FP8: fp32 scales, box 4 x 64 rows (one page)
   size_t scl_off;            // 4-bit: the scales' offset in a page (block scales, then token scales)
 };
@@ -614,6 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
   using PT = typename std::conditional<kConv, __half2, __nv_bfloat162>::type;  // P element pair
   constexpr int kConvThreads = 32 * L::ConvWarps;  // threads converting one ring's units
   constexpr uint32_t kIdescQK = idesc(128, 256, false, false, kConv);
+  constexpr uint32_t kIdescQKb = idesc(128, 256, false, false, false);  // 4-bit cache, k^R unit: bf16 operands
   constexpr uint32_t kIdescPV = idesc(128, 256, false, true, kConv);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -946,13 +959,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
       // ------------------------------------ 4-bit: conversion of both rings' units
       // One rolled loop serves the QK and the PV converters (measured: with the
       // loops apart and unrolled, a third of all warp stalls were instruction
-      // fetches).  A staging slot feeds two units; thread ct takes 32 columns
-      // (two blocks) of row ct / 2 in each of a unit's two 8 KB halves: the two
-      // pages of a QK unit, the two 64-column atoms of a PV unit.
+      // fetches).  A staging slot feeds two units; thread ct takes 32 columns q
+      // (two blocks) of one row in each of a unit's two 8 KB halves: the two
+      // pages of a QK unit, the two 64-column atoms of a PV unit.  Eight lanes
+      // take eight rows, so that the 64-byte swizzle of the staged codes and the
+      // 128-byte swizzle of the operands both spread them over all banks.
       const bool pv = warp >= L::PVConvWarp;
-      constexpr int kHalves = 8 / L::ConvWarps;  // halves of a unit per thread
       const int ct = (warp - (pv ? L::PVConvWarp : L::QKConvWarp)) * 32 + lane;
-      const int row = (ct >> 1) & 63, q = ct & 1, a0 = ct >> 7;
+      const int row = (ct >> 4) * 8 + (ct & 7), q = (ct >> 3) & 1;
       const uint32_t u0 = (uint32_t)(4 * q) ^ (row & 7);
       const uint32_t st_full = bar(pv ? L::PST_FULL : L::QST_FULL), st_empty = bar(pv ? L::PST_EMPTY : L::QST_EMPTY);
       const uint32_t un_empty = bar(pv ? L::PV_EMPTY : L::QK_EMPTY);
@@ -963,9 +977,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
       uint8_t* const ring = smem + (pv ? L::OffPVRing : L::OffQKRing) + row * 128;
       const uint8_t* const st_base = smem + (pv ? L::OffPSt : L::OffQSt);
       const uint32_t st_bytes = pv ? L::PStBytes : kStageBytes;
-      // byte strides of the unit (u) and the half (a) in the staged codes and the scales
-      const uint32_t code_u = pv ? 4096 : 32, code_a = pv ? 32 : 4096;
-      const uint32_t scl_u = pv ? 16 : 4, scl_a = pv ? 4 : L::PageScl, ts_a = pv ? 0 : L::PageScl;
+      // staged codes: 16-byte piece 2 x + q of a 64-byte row, x the unit (QK) or
+      // the half (PV); 4096-byte box the half (QK) or the unit (PV)
+      const uint32_t x0 = (uint32_t)(q ^ ((row >> 1) & 3)) << 4, x1 = x0 ^ 32u;
+      // the two 8-byte groups of block scales: the halves' pages (QK), the units' columns (PV)
+      const uint32_t scl_g = pv ? 16 : L::PageScl, ts_a = pv ? 0 : L::PageScl;
       RingPos unit, stage;
       uint32_t gt = 0;
       SegmentWalker walk(p, w, t);
@@ -992,33 +1008,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
             ok = mbar_wait(st_full + 8 * stage.slot, stage.phase, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
             if (!ok) break;
-            const uint8_t* const src = st_base + stage.slot * st_bytes + row * 64 + q * 16;
+            const uint8_t* const src = st_base + stage.slot * st_bytes + row * 64;
             const uint8_t* const scl = pv ? st_base + stage.slot * st_bytes + kStageBytes : scl_t;
-            const uint8_t* const sclr = scl + row * 32 + 2 * q + (pv ? 8 * (int)rank : 8 * c);
+            const uint8_t* const sclr = scl + row * 32 + (pv ? 8 * (int)rank : 8 * c);
             const uint8_t* const tsr = scl + 2048 + row * 4;
+            uint2 g0 = *reinterpret_cast<const uint2*>(sclr), g1 = *reinterpret_cast<const uint2*>(sclr + scl_g);
+            __half2 ts[2] = {__float2half2_rn(*reinterpret_cast<const float*>(tsr)),
+                             __float2half2_rn(*reinterpret_cast<const float*>(tsr + ts_a))};
+            if (!live) {  // zero scales: the codes of rows past the end may be anything
+              g0 = g1 = make_uint2(0, 0);
+              ts[0] = ts[1] = __float2half2_rn(0.f);
+            }
+            const uint32_t m01 = pv ? g0.y : g1.x, m10 = pv ? g1.x : g0.y;  // (unit, half)
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-              uint4 v[kHalves];
-              uint32_t sc[kHalves];
-              float ts[kHalves];
-#pragma unroll
-              for (int h = 0; h < kHalves; ++h) {
-                const int a = kHalves == 2 ? h : a0;
-                v[h] = *reinterpret_cast<const uint4*>(src + u * code_u + a * code_a);
-                sc[h] = *reinterpret_cast<const uint16_t*>(sclr + u * scl_u + a * scl_a);
-                ts[h] = *reinterpret_cast<const float*>(tsr + a * ts_a);
-              }
+              const uint4 v[2] = {*reinterpret_cast<const uint4*>(src + (pv ? u * 4096 + x0 : u ? x1 : x0)),
+                                  *reinterpret_cast<const uint4*>(src + (pv ? u * 4096 + x1 : 4096 + (u ? x1 : x0)))};
+              const uint32_t sc[2] = {u ? m10 : g0.x, u ? g1.y : m01};
               ok = mbar_wait(un_empty + 8 * unit.slot, unit.phase ^ 1, abort_flag, p.status);
               ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
               if (!ok) break;
               uint8_t* const dst = ring + unit.slot * kUnitBytes;
 #pragma unroll
-              for (int h = 0; h < kHalves; ++h) {
-                const int a = kHalves == 2 ? h : a0;
+              for (int a = 0; a < 2; ++a) {
                 __half2 s0, s1;
-                fp4_block_scales(sc[h], __float2half2_rn(ts[h]), s0, s1);
-                if (!live) s0 = s1 = __float2half2_rn(0.f);
-                store_e2m1x32(dst + a * 8192, u0, v[h], s0, s1);
+                fp4_block_scales((sc[a] >> (16 * q)) & 0xFFFFu, ts[a], s0, s1);
+                store_e2m1x32(dst + a * 8192, u0, v[a], s0, s1);
               }
               fence_proxy_async();
               __syncwarp();
@@ -1031,35 +1046,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
           }
           if (!ok) break;
           if (!pv) {
-            // k^R: one staged page (64 rows x 64 bf16) per half of the unit
+            // k^R unit: bf16 rows by TMA into the ring slot, one box per page; the
+            // first warp's arrival on the leader carries both CTAs' bytes
             ok = mbar_wait(un_empty + 8 * unit.slot, unit.phase ^ 1, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
             if (!ok) break;
-#pragma unroll 1
-            for (int a = 0; a < 2 && ok; ++a) {
-              ok = mbar_wait(st_full + 8 * stage.slot, stage.phase, abort_flag, p.status);
-              ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
-              if (!ok) break;
-              const uint8_t* const src = st_base + stage.slot * st_bytes;
-              uint8_t* const dst = smem + L::OffQKRing + unit.slot * kUnitBytes + a * 8192;
-#pragma unroll
-              for (int k = 0; k < 2 * kHalves; ++k) {
-                const int r = (ct >> 3) + kConvThreads / 8 * k, u = ct & 7;
-                const uint4 x = *reinterpret_cast<const uint4*>(src + r * 128 + u * 16);
-                *reinterpret_cast<uint4*>(dst + r * 128 + ((u ^ (r & 7)) * 16)) =
-                    make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive_local(st_empty + 8 * stage.slot);
-              stage.advance(st_slots);
-            }
-            if (!ok) break;
-            fence_proxy_async();
-            __syncwarp();
             if (lane == 0) {
-              mbar_arrive_cluster(un_full + 8 * unit.slot);
+              const uint32_t fb = un_full + 8 * unit.slot;
+              if (ct == 0) {
+                if (rank == 0) mbar_expect_tx(bar(L::QK_FULL + unit.slot), 2 * kUnitBytes);
+                else mbar_arrive_cluster(fb);
+                for (int i = 0; i < 2; ++i) {
+                  const int tp = tile_page(2 * (int)rank + i);
+                  tma_load_3d_pair(sbase + L::OffQKRing + unit.slot * kUnitBytes + i * 8192, &P.map_kr, 0, 0,
+                                   tp < npg ? page_of(s.b, pg0 + tp) : -1, fb);
+                }
+              } else {
+                mbar_arrive_cluster(fb);
+              }
               mbar_arrive_local(bar(L::SCL_EMPTY + (gt & 1)));
             }
+            __syncwarp();
             unit.advance(un_slots);
           }
         }
@@ -1391,7 +1398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
                 mbar_arrive_tx_local(fb, kStageBytes);
                 for (int i = 0; i < 2; ++i)
                   tma_load_3d(dst + i * 4096, &P.map_codes_qk, kFp4 ? 32 * c : 64 * c, 0, pg[i], fb);
-              } else {
+              } else if (!kFp4) {
                 // k^R: one staging slot per page
                 for (int i = 0; i < 2; ++i) {
                   uint32_t slot;
@@ -1434,7 +1441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
                 if constexpr (kFp4) {
                   const uint32_t fb = bar(L::PST_FULL + slot);
                   const uint32_t dst = sbase + L::OffPSt + slot * L::PStBytes;
-                  mbar_arrive_tx_local(fb, valid > 0 ? L::PStBytes : kStageBytes);
+                  mbar_arrive_tx_local(fb, kStageBytes + (valid > 0 ? L::PageScl : 0));
                   for (int jj = 0; jj < 2; ++jj)
                     tma_load_3d(dst + jj * 4096, &P.map_codes_pv, (256 * jj + x_pv) / 2, 0, valid > 0 ? page : -1, fb);
                   if (valid > 0)  // (no key of the page visible: the converters read no scale)
@@ -1522,7 +1529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
               const uint64_t a = qdesc + 512 * c, bb = kdesc + 1024 * ring.pos.slot;
 #pragma unroll
               for (int k4 = 0; k4 < 4; ++k4)  // 16 columns = 32 bytes into the swizzled rows
-                tc_mma(sd, a + 2 * k4, bb + 2 * k4, kIdescQK, (c | k4) ? 1u : 0u);
+                tc_mma(sd, a + 2 * k4, bb + 2 * k4, kFp4 && c == kChunks - 1 ? kIdescQKb : kIdescQK, (c | k4) ? 1u : 0u);
               ring.release();
             }
             if (!ok) break;
@@ -1668,10 +1675,11 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows
          CUDA_SUCCESS;
 }
 
-// 3-D map over a page sub-block: [pages][64 rows][row_elems], unswizzled box
+// 3-D map over a page sub-block: [pages][64 rows][row_elems], box
 // (box_x x 64 rows x 1 page)
 bool make_page_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint32_t elem_bytes,
-                   uint64_t row_elems, uint64_t num_pages, uint64_t page_bytes, uint32_t box_x) {
+                   uint64_t row_elems, uint64_t num_pages, uint64_t page_bytes, uint32_t box_x,
+                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[3] = {row_elems, (cuuint64_t)kPage, num_pages};
@@ -1679,7 +1687,7 @@ bool make_page_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, u
   const cuuint32_t box[3] = {box_x, (cuuint32_t)kPage, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
 
@@ -1723,6 +1731,7 @@ bool decode_tc_supported(const mla_dims& d, int n_q) {
 }
 
 bool decode_tc_wants_f16_queries(const mla_dims& d) { return is_coded_cache(d); }
+bool decode_tc_wants_bf16_q_rope(const mla_dims& d) { return d.cache_dtype == MLA_FP4_E2M1; }
 
 int decode_tc_auto_splits(int num_sms, int n_q) {
   const int pairs = num_sms / 2;
@@ -1741,9 +1750,9 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st) {
     tp.scl_off = f4.sc_off;
     if (!make_map(&tp.map_q, p.q_abs, q_rows, 64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) ||
         !make_page_map(&tp.map_codes_pv, p.pool, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kDC / 2, p.num_pages, p.page_bytes,
-                       64) ||
+                       64, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !make_page_map(&tp.map_kr, p.pool + f4.kr_off, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kDR, p.num_pages,
-                       p.page_bytes, 64))
+                       p.page_bytes, 64, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
     tp.map_codes_qk = tp.map_codes_pv;
     return launch_variant<MLA_FP4_E2M1>(tp, p.splits * p.n_q, st);

@@ -344,7 +344,7 @@ cudaError_t launch_append_fp4_finalize(const mla_dims& d, const float* raw, int 
 // absorb + split plan (+ empty-split initialisation of the lse slots)
 cudaError_t launch_absorb_and_plan(const mla_dims& d, const void* q_nope, const void* q_rope, const void* W_uk,
                                    const int32_t* seq_lens, int batch, int n_q, int max_pages, int splits,
-                                   void* q_abs, bool q_abs_f16, int32_t* plan, float* lse_part, size_t lse_count,
+                                   void* q_abs, bool q_abs_f16, bool q_rope_bf16, int32_t* plan, float* lse_part, size_t lse_count,
                                    int* status, cudaStream_t st);
 
 cudaError_t launch_decode_simt(const DecodeParams& p, cudaStream_t st);
@@ -352,6 +352,8 @@ cudaError_t launch_decode_simt(const DecodeParams& p, cudaStream_t st);
 bool decode_tc_supported(const mla_dims& d, int n_q);
 // the tensor-core path for this cache reads the absorbed queries as f16
 bool decode_tc_wants_f16_queries(const mla_dims& d);
+// ... but for the rotated q^R, which it reads as bf16 beside a bf16 k^R
+bool decode_tc_wants_bf16_q_rope(const mla_dims& d);
 // multiprocessor count of the current device (cached per device)
 int device_sm_count();
 
