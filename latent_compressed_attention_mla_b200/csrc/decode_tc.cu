@@ -131,7 +131,9 @@ struct TcLayout {
   static constexpr int SCL_FULL = PST_EMPTY + PStSlots;  // [SclBufs] local: a tile's scales landed
   static constexpr int SCL_EMPTY = SCL_FULL + SclBufs;   // [SclBufs] local: all converter warps done
   static constexpr int DRAIN = SCL_EMPTY + SclBufs;      // each CTA: both MMA issuers' operations completed
-  static constexpr int NumBars = DRAIN + 1;
+  static constexpr int P_FULL2 = DRAIN + 1;              // 4-bit, leader: P of key positions 2 and 3 written
+  static constexpr int P_FREE = P_FULL2 + 1;             // 4-bit, each CTA: the MMAs reading P positions 0 and 1 finished
+  static constexpr int NumBars = P_FREE + 1;
   static constexpr uint32_t OffMisc = OffBar + NumBars * 8;
   static constexpr uint32_t OffRedMax = OffMisc + 16;   // float [2][64]
   static constexpr uint32_t OffRedL = OffRedMax + 512;  // float [2][64]
@@ -678,6 +680,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
       mbar_init(bar(L::SCL_FULL + i), 1);
       mbar_init(bar(L::SCL_EMPTY + i), (kFp4 ? 1 : 2) * L::ConvWarps);
     }
+    mbar_init(bar(L::P_FULL2), 4);
+    mbar_init(bar(L::P_FREE), 1);
     mbar_init(bar(L::DRAIN), 2);  // the QK and the PV issuer's final commit
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -750,7 +754,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
       float m_ref = -INFINITY, l_part = 0.f;
       const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
       for (int it = 0; it < n_tiles; ++it, ++g) {
-        ok = softmax_all_ok(mbar_wait(bar(L::S_FULL + (g & 1)), (g >> 1) & 1, abort_flag, p.status));
+        ok = softmax_all_ok(mbar_wait(bar(L::S_FULL + (g & 1)), (g >> 1) & 1, abort_flag, p.status) && ok);
         if (!ok) break;
         if (threadIdx.x == 0) TC_TRACE(4, g);
         tc_fence_after();
@@ -867,6 +871,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
             }
           }
           release_s();
+          if constexpr (kFp4) {
+            // P is handed over in two halves, so that the tile's PV MMAs start as
+            // soon as the previous tile's end: warps 0-1 (key positions 0 and
+            // 1) overwrite theirs once the MMAs of those positions are done, halfway
+            // through the previous tile's; warps 2-3 once all are.  The first
+            // half's barrier also says that every warp has rescaled its part of
+            // O, which waits for all of the previous tile's MMAs where it happens.
+            // A failed wait is agreed on at the next tile's (or the epilogue's).
+            const bool resc = __any_sync(0xffffffffu, rescale);
+            if (resc) ok = wait_pv_rescale();
+            tc_fence_before();
+            if (half == 1 && lane == 0) mbar_arrive_cluster(leader_bar(L::P_FULL));
+            if (g >= 1 && ok && !resc)
+              ok = __all_sync(0xffffffffu, mbar_wait(bar(half ? L::O_DONE : L::P_FREE), (g - 1) & 1, abort_flag, p.status));
+            if (ok) {
+              store_p(0, pk_lo);
+              store_p(1, pk_hi);
+            }
+            l_part = l_part * alpha + psum;
+            fence_proxy_async();
+            __syncwarp();
+            if (threadIdx.x == 0) TC_TRACE(6, g);
+            if (lane == 0) mbar_arrive_cluster(leader_bar(half ? L::P_FULL2 : L::P_FULL));
+            continue;
+          }
           ok = softmax_all_ok(wait_pv_rescale());
           if (!ok) break;
           store_p(0, pk_lo);
@@ -894,7 +923,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
       }
       if (!ok) break;
       // epilogue: wait for the last PV, normalise, write the split's partial
-      ok = softmax_all_ok(mbar_wait(bar(L::O_DONE), (g - 1) & 1, abort_flag, p.status));
+      ok = softmax_all_ok(mbar_wait(bar(L::O_DONE), (g - 1) & 1, abort_flag, p.status) && ok);
       if (!ok) break;
       tc_fence_after();
       red_l[half * 64 + hl] = l_part;
@@ -1576,7 +1605,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
             tc_fence_after();
             TC_TRACE(2, g);
 #pragma unroll 1
-            for (int i = 0; i < kTilePages && ok; ++i)
+            for (int i = 0; i < kTilePages && ok; ++i) {
+              if (kFp4 && i == 2) {  // P of the upper key positions comes on its own
+                ok = mbar_wait(bar(L::P_FULL2), g & 1, abort_flag, p.status);
+                if (!ok) break;
+                tc_fence_after();
+              }
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
 #ifdef MLA_TC_TRACE
@@ -1594,6 +1628,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
                          vdesc + 1024 * ring.pos.slot + 128 * ks, kIdescPV, (it == 0 && i == 0 && ks == 0) ? 0u : 1u);
                 ring.release();
               }
+              if (kFp4 && i == 1 && ok) tc_commit_pair(bar(L::P_FREE));
+            }
             if (!ok) break;
             tc_commit_pair(bar(L::O_DONE));
             TC_TRACE(3, g);
