@@ -1028,6 +1028,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
           }
           const int pg0 = s.page_lo + it * kTilePages;
           const int npg = min(kTilePages, s.n_pages - it * kTilePages);
+          // pages of the k^R unit (looked up here, loaded at the tile's end)
+          int kr_page[2] = {-1, -1};
+          if (!pv && ct == 0)
+            for (int i = 0; i < 2; ++i) {
+              const int tp = tile_page(2 * (int)rank + i);
+              if (tp < npg) kr_page[i] = page_of(s.b, pg0 + tp);
+            }
 #pragma unroll 1
           for (int c = 0; c < 4 && ok; ++c) {
             // QK: columns [128 c, 128 c + 128) of this CTA's two pages.  PV: key
@@ -1085,11 +1092,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
               if (ct == 0) {
                 if (rank == 0) mbar_expect_tx(bar(L::QK_FULL + unit.slot), 2 * kUnitBytes);
                 else mbar_arrive_cluster(fb);
-                for (int i = 0; i < 2; ++i) {
-                  const int tp = tile_page(2 * (int)rank + i);
+                for (int i = 0; i < 2; ++i)
                   tma_load_3d_pair(sbase + L::OffQKRing + unit.slot * kUnitBytes + i * 8192, &P.map_kr, 0, 0,
-                                   tp < npg ? page_of(s.b, pg0 + tp) : -1, fb);
-                }
+                                   kr_page[i], fb);
               } else {
                 mbar_arrive_cluster(fb);
               }

@@ -76,7 +76,10 @@ int check_dims(const mla_dims* d) {
 int auto_splits(const mla_dims& d, int batch, int n_q) {
   (void)batch;
   const int sms = num_sms();
-  if (!(d.flags & MLA_FLAG_FORCE_SIMT) && decode_tc_supported(d, n_q)) return decode_tc_auto_splits(sms, n_q);
+  if (!(d.flags & MLA_FLAG_FORCE_SIMT)) {
+    if (decode_tc_supported(d, n_q)) return decode_tc_auto_splits(sms, n_q);
+    if (decode_few_supported(d, n_q)) return decode_few_auto_splits(d, sms, n_q);
+  }
   const int hg = d.n_heads % 8 == 0 && d.d_c / 16 <= 32 ? 8 : 4;
   const int groups = d.n_heads / hg;  // 0 where no SIMT kernel takes these heads either
   const int per_split = n_q * (groups > 0 ? groups : 1);
@@ -150,7 +153,10 @@ size_t mla_decode_workspace_bytes(const mla_dims* dims, int batch, int n_q, int 
 int mla_decode_path(const mla_dims* dims, int n_q) {
   int rc = check_dims(dims);
   if (rc != MLA_OK) return -rc;
-  if (!(dims->flags & MLA_FLAG_FORCE_SIMT) && decode_tc_supported(*dims, n_q)) return 1;
+  if (!(dims->flags & MLA_FLAG_FORCE_SIMT)) {
+    if (decode_tc_supported(*dims, n_q)) return 1;
+    if (decode_few_supported(*dims, n_q)) return 2;
+  }
   return decode_simt_supported(*dims) ? 0 : -MLA_ERR_UNSUPPORTED;
 }
 
@@ -185,7 +191,7 @@ int mla_decode(const mla_dims* dims, const void* q_nope, const void* q_rope, con
   int* status = status_ptr();
   trace_record(MLA_TRACE_ABSORB, false, st);
   const int n_slots = batch + W - 1;
-  const bool q_f16 = path == 1 && decode_tc_wants_f16_queries(*dims);
+  const bool q_f16 = path >= 1 && decode_tc_wants_f16_queries(*dims);
   cudaError_t e = launch_absorb_and_plan(*dims, q_nope, q_rope, W_uk, seq_lens, batch, n_q, max_pages, W, ws + L.off_q,
                                          q_f16, q_f16 && decode_tc_wants_bf16_q_rope(*dims), plan, reinterpret_cast<float*>(ws + L.off_lse),
                                          (size_t)n_q * n_slots * dims->n_heads, status, st);
@@ -211,7 +217,7 @@ int mla_decode(const mla_dims* dims, const void* q_nope, const void* q_rope, con
   p.status = status;
   p.timeline = timeline_ptr();
   trace_record(MLA_TRACE_ATTEND, false, st);
-  e = path == 1 ? launch_decode_tc(p, st) : launch_decode_simt(p, st);
+  e = path == 1 ? launch_decode_tc(p, st) : path == 2 ? launch_decode_few(p, st) : launch_decode_simt(p, st);
   trace_record(MLA_TRACE_ATTEND, true, st);
   return launch_status(e);
 }
@@ -229,7 +235,7 @@ int mla_combine(const mla_dims* dims, const void* W_uv, int batch, int n_q, int 
   const uint8_t* ws = static_cast<const uint8_t*>(workspace);
   trace_record(MLA_TRACE_COMBINE, false, (cudaStream_t)stream);
   // the partials' row type follows the decode path that wrote them
-  const bool part_bf16 = mla_decode_path(dims, n_q) == 1;
+  const bool part_bf16 = mla_decode_path(dims, n_q) >= 1;
   cudaError_t e = launch_combine(*dims, W_uv, batch, n_q, reinterpret_cast<const int32_t*>(ws + L.off_plan),
                                  reinterpret_cast<const float*>(ws + L.off_o), part_bf16,
                                  reinterpret_cast<const float*>(ws + L.off_lse), out, lse_out, status_ptr(),

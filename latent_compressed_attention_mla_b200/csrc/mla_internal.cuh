@@ -98,6 +98,12 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 bool make_tile_map_bf16(void* map, const void* base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
                         uint32_t box_cols, uint32_t box_rows);
 
+// 3-D map over a sub-block of the cache pages, [pages][rows][row_elems] of bytes
+// or bf16, one page's rows x box_cols per box, 128-byte swizzle (a box row is
+// 128 bytes).
+bool make_page_map_swizzled(void* map, const void* base, bool bf16, uint64_t row_elems, uint64_t rows, uint64_t pages,
+                            uint64_t page_bytes, uint32_t box_cols);
+
 // ----------------------------------------------------------------------------
 // Element access
 // ----------------------------------------------------------------------------
@@ -396,6 +402,10 @@ __device__ __forceinline__ void mla_stamp_now(int e) {
 #define MLA_STAMP_EXPORT(unit)
 #endif
 cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st);
+// few query rows over a 4-bit cache, warp-level tensor cores (decode_few.cu)
+bool decode_few_supported(const mla_dims& d, int n_q);
+int decode_few_auto_splits(const mla_dims& d, int num_sms, int n_q);
+cudaError_t launch_decode_few(const DecodeParams& p, cudaStream_t st);
 int decode_tc_auto_splits(int num_sms, int n_q);
 
 // part_bf16: the split partials are bf16 rows (the tensor-core decode writes

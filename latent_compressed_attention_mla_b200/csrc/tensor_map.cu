@@ -38,6 +38,20 @@ bool make_tile_map_bf16(void* map, const void* base, uint64_t cols, uint64_t row
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_page_map_swizzled(void* map, const void* base, bool bf16, uint64_t row_elems, uint64_t rows, uint64_t pages,
+                            uint64_t page_bytes, uint32_t box_cols) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {row_elems, rows, pages};
+  const cuuint64_t strides[2] = {row_elems * (bf16 ? 2 : 1), page_bytes};
+  const cuuint32_t box[3] = {box_cols, (cuuint32_t)rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(static_cast<CUtensorMap*>(map), bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
 int device_sm_count() {
   constexpr int kMaxDev = 64;
   static int cached[kMaxDev] = {};
