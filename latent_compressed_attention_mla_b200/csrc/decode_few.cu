@@ -64,8 +64,8 @@ struct Layout {
   static constexpr uint32_t OffQ = OffScl + Stages * kTilePages * kSclBytes;  // [MT][4 dq][kSteps][32 lanes] fragments
   static constexpr uint32_t OffX = OffQ + MT * 4 * kSteps * 512;             // [MT][kWarps][4][32 lanes] float4
   static constexpr uint32_t OffP = OffX + MT * kWarps * 4 * 512;             // [Rows][128 keys] f16, 16-byte units swizzled
-  static constexpr uint32_t OffMax = OffP + Rows * kTileKeys * 2;            // int [2][Rows]
-  static constexpr uint32_t OffL = OffMax + 2 * Rows * 4;                    // float [kWarps][Rows]
+  static constexpr uint32_t OffMax = OffP + Rows * kTileKeys * 2;            // int [Rows]
+  static constexpr uint32_t OffL = OffMax + Rows * 4;                    // float [kWarps][Rows]
   static constexpr uint32_t OffBar = OffL + kWarps * Rows * 4;
   static constexpr uint32_t Bytes = OffBar + Stages * 8 + 1024;              // + alignment slack
 };
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
   pdl_trigger();
   if (tid == 0)
     for (int s = 0; s < L::Stages; ++s) mbar_init_local(bar(s), 1);
-  if (tid < 2 * L::Rows) s_max[tid] = float_order(-INFINITY);
+  if (tid < L::Rows) s_max[tid] = float_order(-INFINITY);
   __syncthreads();
   pdl_wait();
   tl_begin(p.timeline, MLA_TRACE_ATTEND);
@@ -175,41 +175,66 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
   // loads: lane i of warp 0 brings page i of a tile; the walker runs ahead of the tiles
   PieceWalker lwalk(p, w, t_hi);
   Piece lp;
-  int l_at = 0, l_stage = 0;
+  int l_at = 0, l_stage = 0, l_page = 0;
   lp.n_pages = 0;
   const bool stall = (p.d.flags & MLA_FLAG_SELFTEST_STALL) != 0;
-  auto load_next = [&]() {  // warp 0
+  // the next tile's page of this lane (looked up one load ahead)
+  auto look_up = [&]() {
     while (l_at >= lp.n_pages) {
-      if (!lwalk.next(lp)) return;
+      lp.n_pages = 0;
       l_at = 0;
+      if (!lwalk.next(lp)) return;
     }
+    if (lane < min(kTilePages, lp.n_pages - l_at))
+      l_page = p.page_table[(size_t)lp.b * p.max_pages + lp.page_lo + l_at + lane];
+  };
+  auto load_next = [&]() {  // warp 0
+    if (lp.n_pages == 0) return;  // no tile left
     const int npg = min(kTilePages, lp.n_pages - l_at);
-    if (lane == 0 && !stall) mbar_expect_local(bar(l_stage), npg * (kCodeBytes + kKrBytes + kSclBytes));
-    __syncwarp();
-    if (lane < npg && !stall) {
-      int page = p.page_table[(size_t)lp.b * p.max_pages + lp.page_lo + l_at + lane];
-      if (page < 0 || page >= p.num_pages) {
-        record_status(p.status, MLA_ERR_BOUNDS);
-        page = 0;
+    if (!stall) {
+      if (lane == 0) mbar_expect_local(bar(l_stage), npg * (kCodeBytes + kKrBytes + kSclBytes));
+      __syncwarp();
+      if (lane < npg) {
+        int page = l_page;
+        if (page < 0 || page >= p.num_pages) {
+          record_status(p.status, MLA_ERR_BOUNDS);
+          page = 0;
+        }
+        const uint32_t st = sbase + L::OffStage + l_stage * kStageBytes, fb = bar(l_stage);
+        for (int h = 0; h < 2; ++h)
+          tma_load_3d(st + lane * kCodeBytes + h * (kCodeBytes / 2), &P.map_codes, 128 * h, 0, page, fb);
+        tma_load_3d(st + kTilePages * kCodeBytes + lane * kKrBytes, &P.map_kr, 0, 0, page, fb);
+        bulk_load(sbase + L::OffScl + (l_stage * kTilePages + lane) * kSclBytes,
+                  p.pool + (size_t)page * p.page_bytes + P.scl_off, kSclBytes, fb);
       }
-      const uint32_t st = sbase + L::OffStage + l_stage * kStageBytes, fb = bar(l_stage);
-      for (int h = 0; h < 2; ++h)
-        tma_load_3d(st + lane * kCodeBytes + h * (kCodeBytes / 2), &P.map_codes, 128 * h, 0, page, fb);
-      tma_load_3d(st + kTilePages * kCodeBytes + lane * kKrBytes, &P.map_kr, 0, 0, page, fb);
-      bulk_load(sbase + L::OffScl + (l_stage * kTilePages + lane) * kSclBytes,
-                p.pool + (size_t)page * p.page_bytes + P.scl_off, kSclBytes, fb);
+      __syncwarp();
     }
-    __syncwarp();
     l_at += npg;
     if (++l_stage == L::Stages) l_stage = 0;
+    look_up();
   };
+  if (warp == 0) look_up();
   if (warp == 0)
     for (int s = 0; s < L::Stages; ++s) load_next();
 
   const int kg = warp >> 2, dq = warp & 3;  // scores, softmax
   const int ds = warp & 7, kh = warp >> 3;  // values
-  int stage = 0;
-  uint32_t phase = 0, tile = 0;
+  // This thread's places in a staged tile; the loops add multiples of eight
+  // rows, which leave the swizzle as it is.
+  const int qk_key = (32 * kg & 63) + key_of(g);  // scores: row of page kg / 2, + 8 nt
+  const uint32_t qk_codes = (uint32_t)((kg >> 1) * kCodeBytes + (dq >> 1) * (kCodeBytes / 2) + qk_key * 128 +
+                                       ((((dq & 1) * 4 + q) ^ (qk_key & 7)) << 4));
+  const uint32_t qk_kr = (uint32_t)(kTilePages * kCodeBytes + (kg >> 1) * kKrBytes + qk_key * 128 +
+                                    (((2 * q + (dq >> 1)) ^ (qk_key & 7)) << 4) + (dq & 1) * 8);
+  const uint32_t qk_scl = (uint32_t)((kg >> 1) * kSclBytes + qk_key * 32 + 8 * dq + 2 * q);
+  const uint32_t qk_ts = (uint32_t)((kg >> 1) * kSclBytes + kPage * kDC / 16 + (32 * kg & 63) * 4);
+  const int k0 = 2 * q, k1 = key_of(2 * q + 1);   // keys of an accumulator's columns, of a value fragment's halves
+  const uint32_t pv_col = (ds & 3) * 2 + (g >> 2);
+  const uint32_t pv_box = (uint32_t)(kh * kCodeBytes + (ds >> 2) * (kCodeBytes / 2) + (g & 3) * 4);
+  const uint32_t pv_codes0 = pv_box + k0 * 128 + ((pv_col ^ k0) << 4), pv_codes1 = pv_box + k1 * 128 + ((pv_col ^ k1) << 4);
+  const uint32_t pv_scl = (uint32_t)(kh * kSclBytes + 4 * ds + (g >> 1));
+  int qk_stage = 0, pv_stage = 0;
+  uint32_t qk_phase = 0;
   bool ok = true;
   PieceWalker walk(p, w, t_hi);
   Piece s;
@@ -254,16 +279,32 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
       }
     }
     const int nvis_lo = min(s.len - p.n_q + t_lo + 1, s.end), nvis_hi = min(s.len - p.n_q + t_hi + 1, s.end);
-    for (int at = 0; at < s.n_pages; at += kTilePages, ++tile) {
-      const int key0 = (s.page_lo + at) * kPage;
-      const int n_keys = nvis_hi - key0;  // keys of the tile that some row sees (more than 127: all)
-      const bool tail = key0 + kTileKeys > nvis_lo;  // some key of the tile is hidden from some row
-      const uint8_t* st = smem + L::OffStage + stage * kStageBytes;
-      const uint8_t* scl = smem + L::OffScl + stage * kTilePages * kSclBytes;
-      ok = mbar_wait_bounded(bar(stage), phase);
-      // ------------------------------------------------------------ scores
-      float acc[MT][4][4];
-      {
+    const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
+    // Pipeline: the scores of tile i + 1 and the values of tile i share a phase
+    // (either's latencies lie under the other's work), the softmax of i + 1 follows.
+    for (int i = -1; i < n_tiles; ++i) {
+      const bool more = i + 1 < n_tiles;
+      const int key0 = (s.page_lo + (i + 1) * kTilePages) * kPage;  // tile i + 1
+      const bool tail = key0 + kTileKeys > nvis_lo;  // some key of it is hidden from some row
+      float4* X = reinterpret_cast<float4*>(smem + L::OffX);
+      // ------------------------------------------------ scores of tile i + 1
+      if (more) {
+        const uint8_t* st = smem + L::OffStage + qk_stage * kStageBytes;
+        uint8_t* scl = smem + L::OffScl + qk_stage * kTilePages * kSclBytes;
+        ok = mbar_wait_bounded(bar(qk_stage), qk_phase) && ok;
+        if (tail) {
+          // keys that no row sees count as zero, whatever the page holds there
+          const int n_keys = nvis_hi - key0;
+          for (int k = tid >> 2; k < kTileKeys; k += kThreads / 4)
+            if (k >= n_keys) {
+              uint8_t* ps = scl + (k >> 6) * kSclBytes;
+              *reinterpret_cast<uint2*>(ps + (k & 63) * 32 + 8 * (tid & 3)) = make_uint2(0, 0);
+              if ((tid & 3) == 0) *reinterpret_cast<float*>(ps + kPage * kDC / 16 + (k & 63) * 4) = 1.0f;
+            }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a later load overwrites them
+          __syncthreads();
+        }
+        float acc[MT][4][4];
         uint4 v[4];
         __half2 sc[4][2];
         const uint4* qf = reinterpret_cast<const uint4*>(smem + L::OffQ) + dq * kSteps * 32 + lane;
@@ -272,22 +313,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
         for (int mt = 0; mt < MT; ++mt) qr[mt] = qf[(mt * 4 * kSteps + 8) * 32];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-          const int key = 32 * kg + 8 * nt + key_of(g), pg = key >> 6, row = key & 63;
-          const uint8_t* ps = scl + pg * kSclBytes;
-          // k^R columns 16 q + 4 dq .. + 3
-          const uint2 kr = *reinterpret_cast<const uint2*>(
-              st + kTilePages * kCodeBytes + pg * kKrBytes + row * 128 + (((2 * q + (dq >> 1)) ^ (row & 7)) << 4) + (dq & 1) * 8);
-          v[nt] = *reinterpret_cast<const uint4*>(st + pg * kCodeBytes + (dq >> 1) * (kCodeBytes / 2) + row * 128 +
-                                                  ((((dq & 1) * 4 + q) ^ (row & 7)) << 4));
+          const uint2 kr = *reinterpret_cast<const uint2*>(st + qk_kr + nt * 1024);
+          v[nt] = *reinterpret_cast<const uint4*>(st + qk_codes + nt * 1024);
           const __half2 s2 = __half2(__nv_cvt_fp8x2_to_halfraw2(
-              *reinterpret_cast<const uint16_t*>(ps + row * 32 + 8 * dq + 2 * q), __NV_E4M3));
+              *reinterpret_cast<const uint16_t*>(scl + qk_scl + nt * 256), __NV_E4M3));
           sc[nt][0] = __low2half2(s2);
           sc[nt][1] = __high2half2(s2);
           // (q^R . k^R) / ts of the accumulator's two keys
-          const float* ts = reinterpret_cast<const float*>(scl + ((32 * kg + 8 * nt) >> 6) * kSclBytes + kPage * kDC / 16) +
-                            ((32 * kg + 8 * nt) & 63);
-          const float i0 = __uint_as_float(0x7F000000u - __float_as_uint(ts[2 * q]));
-          const float i1 = __uint_as_float(0x7F000000u - __float_as_uint(ts[key_of(2 * q + 1)]));
+          const uint32_t* ts = reinterpret_cast<const uint32_t*>(scl + qk_ts) + 8 * nt;
+          const float i0 = __uint_as_float(0x7F000000u - ts[k0]), i1 = __uint_as_float(0x7F000000u - ts[k1]);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
@@ -319,31 +353,75 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
             }
           }
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+            X[((mt * kWarps + warp) * 4 + nt) * 32 + lane] =
+                make_float4(acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]);
       }
-      float4* X = reinterpret_cast<float4*>(smem + L::OffX);
+      // ---------------------------------------------------- values of tile i
+      if (i >= 0) {
+        const uint8_t* st = smem + L::OffStage + pv_stage * kStageBytes;
+        const uint8_t* scl = smem + L::OffScl + pv_stage * kTilePages * kSclBytes;
+        // thread: columns 64 ds + 8 g .. + 7 of keys 16 kb + {k0, k1} and 8 more; the
+        // codes of the two keys are interleaved, so that a byte converts into
+        // the f16 pair of one column, and the pair of scales multiplies it
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        for (int kb = 0; kb < 4; ++kb) {
+          uint4 pa[MT];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-          X[((mt * kWarps + warp) * 4 + nt) * 32 + lane] =
-              make_float4(acc[mt][nt][0], acc[mt][nt][1], acc[mt][nt][2], acc[mt][nt][3]);
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + kg) : "memory");  // the four quarters of key group kg
-      // ----------------------------------------------------------- softmax
-      // keys 32 kg + 8 dq + {2q, key_of(2q + 1)}; rows 16 mt + g, + 8
-      float x[MT][4];
-      float inv_ts[2];
+          for (int mt = 0; mt < MT; ++mt) {
+            const int r = 16 * mt + (lane & 15), u = 8 * kh + 2 * kb + (lane >> 4);
+            ldsm_x4(sbase + L::OffP + r * 256 + ((u ^ (r & 7)) << 4), pa[mt].x, pa[mt].y, pa[mt].z, pa[mt].w);
+          }
+          uint32_t b0[8], b1[8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // keys 16 kb + 8 h + {k0, k1}
+            const uint32_t w0 = *reinterpret_cast<const uint32_t*>(st + pv_codes0 + kb * 2048 + h * 1024);
+            const uint32_t w1 = *reinterpret_cast<const uint32_t*>(st + pv_codes1 + kb * 2048 + h * 1024);
+            const uint32_t s0 = scl[pv_scl + k0 * 32 + kb * 512 + h * 256], s1 = scl[pv_scl + k1 * 32 + kb * 512 + h * 256];
+            const __half2 s2 = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(s0 | (s1 << 8)), __NV_E4M3));
+            __half2 he[4], ho[4];  // columns 0, 2, 4, 6 and 1, 3, 5, 7
+            e2m1x8_to_half2((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), he);
+            e2m1x8_to_half2(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), ho);
+            uint32_t* bb = h ? b1 : b0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              bb[2 * m] = as_u32(__hmul2(he[m], s2));
+              bb[2 * m + 1] = as_u32(__hmul2(ho[m], s2));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][j], pa[mt], b0[j], b1[j]);
+        }
+      }
+      // every warp is done with tile i (its stage and P are free) and has
+      // published its scores of tile i + 1
+      ok = __syncthreads_and(ok);
+      if (!ok) break;
+      if (i >= 0) {
+        pv_stage = pv_stage + 1 == L::Stages ? 0 : pv_stage + 1;
+        if (warp == 0) load_next();
+      }
+      if (!more) break;
+      // ----------------------------------------------- softmax of tile i + 1
+      // keys 32 kg + 8 dq + {k0, k1}; rows 16 mt + g, + 8
+      float x[MT][4], p4[MT][4], inv_ts[2];
       {
         const int k8 = 32 * kg + 8 * dq;
-        const float* ts = reinterpret_cast<const float*>(scl + (k8 >> 6) * kSclBytes + kPage * kDC / 16) + (k8 & 63);
-        const int kk[2] = {2 * q, key_of(2 * q + 1)};
+        const uint32_t* ts =
+            reinterpret_cast<const uint32_t*>(smem + L::OffScl + qk_stage * kTilePages * kSclBytes + qk_ts) + 8 * dq;
+        const int kk[2] = {k0, k1};
         float a[2], e[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const uint32_t u = __float_as_uint(ts[kk[c]]);
+          const uint32_t u = ts[kk[c]];
           a[c] = __uint_as_float(u) * p.scale_log2;
           e[c] = (float)((int)(u >> 23) - 127);
           inv_ts[c] = __uint_as_float(0x7F000000u - u);
-          if (tail && key0 + k8 + kk[c] >= nvis_hi) inv_ts[c] = 0.f;
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -365,84 +443,67 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
             for (int c = 0; c < 4; ++c)
               if (key0 + k8 + kk[c & 1] >= nvis[mt][c >> 1]) x[mt][c] = -INFINITY;
           }
+        }
+      }
+      auto probabilities = [&]() {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float m = m_ref[mt][r] == -INFINITY ? 0.f : m_ref[mt][r];  // a row that sees no key yet
+            p4[mt][2 * r] = fast_exp2(x[mt][2 * r] - m);
+            p4[mt][2 * r + 1] = fast_exp2(x[mt][2 * r + 1] - m);
+            const int row = 16 * mt + 8 * r + g;
+            *reinterpret_cast<__half2*>(smem + L::OffP + row * 256 + (((4 * kg + dq) ^ (row & 7)) << 4) + 4 * q) =
+                __floats2half2_rn(p4[mt][2 * r], p4[mt][2 * r + 1]);
+          }
+      };
+      bool over = false;  // a score passes its row's reference by more than the threshold
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) over |= x[mt][c] > m_ref[mt][c >> 1] + kRescaleThreshold;
+      probabilities();
+      if (__syncthreads_or(over)) {
+        // rare: the rows' maxima over the tile move the references
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             float mx = fmaxf(x[mt][2 * r], x[mt][2 * r + 1]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            if (q == 0) atomicMax(&s_max[(tile & 1) * L::Rows + 16 * mt + 8 * r + g], float_order(mx));
+            if (q == 0) atomicMax(&s_max[16 * mt + 8 * r + g], float_order(mx));
           }
-        }
+        __syncthreads();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float t_max = order_float(s_max[16 * mt + 8 * r + g]);
+            if (t_max > m_ref[mt][r] + kRescaleThreshold) {
+              const float alpha = fast_exp2(m_ref[mt][r] - t_max);
+              m_ref[mt][r] = t_max;
+              l_sum[mt][r] *= alpha;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                o[mt][j][2 * r] *= alpha;
+                o[mt][j][2 * r + 1] *= alpha;
+              }
+            }
+          }
+        probabilities();
+        __syncthreads();
+        if (tid < L::Rows) s_max[tid] = float_order(-INFINITY);
       }
-      // every warp is done with the previous tile: its stage and P are free
-      ok = __syncthreads_and(ok);
-      if (!ok) break;
-      if (warp == 0 && tile > 0) load_next();
-      if (tid >= kThreads - L::Rows) s_max[((tile & 1) ^ 1) * L::Rows + tid - (kThreads - L::Rows)] = float_order(-INFINITY);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float t_max = order_float(s_max[(tile & 1) * L::Rows + 16 * mt + 8 * r + g]);
-          if (t_max > m_ref[mt][r] + kRescaleThreshold) {
-            const float alpha = fast_exp2(m_ref[mt][r] - t_max);
-            m_ref[mt][r] = t_max;
-            l_sum[mt][r] *= alpha;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              o[mt][j][2 * r] *= alpha;
-              o[mt][j][2 * r + 1] *= alpha;
-            }
-          }
-          const float m = m_ref[mt][r] == -INFINITY ? 0.f : m_ref[mt][r];  // a row that sees no key yet
-          const float p0 = fast_exp2(x[mt][2 * r] - m), p1 = fast_exp2(x[mt][2 * r + 1] - m);
-          l_sum[mt][r] = fmaf(p0, inv_ts[0], fmaf(p1, inv_ts[1], l_sum[mt][r]));
-          const int row = 16 * mt + 8 * r + g;
-          *reinterpret_cast<__half2*>(smem + L::OffP + row * 256 + (((4 * kg + dq) ^ (row & 7)) << 4) + 4 * q) =
-              __floats2half2_rn(p0, p1);
-        }
-      __syncthreads();
-      // ------------------------------------------------------------ values
-      // thread: columns 64 ds + 8 g .. + 7 of keys 16 kb + {2q, key_of(2q + 1)} and 8 more
-#pragma unroll 1
-      for (int kb = 4 * kh; kb < 4 * kh + 4; ++kb) {
-        uint4 pa[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int r = 16 * mt + (lane & 15), u = 2 * kb + (lane >> 4);
-          ldsm_x4(smem_addr(smem + L::OffP) + r * 256 + ((u ^ (r & 7)) << 4), pa[mt].x, pa[mt].y, pa[mt].z, pa[mt].w);
-        }
-        const int pg = kb >> 2;
-        const uint8_t* cb = st + pg * kCodeBytes + (ds >> 2) * (kCodeBytes / 2) + (g & 3) * 4;
-        const uint8_t* sb = scl + pg * kSclBytes + 4 * ds + (g >> 1);
-        __half2 h[4][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = (16 * kb & 63) + 8 * (k >> 1) + ((k & 1) ? key_of(2 * q + 1) : 2 * q);
-          const uint32_t word =
-              *reinterpret_cast<const uint32_t*>(cb + row * 128 + ((((ds & 3) * 2 + (g >> 2)) ^ (row & 7)) << 4));
-          uint32_t sbyte = sb[row * 32];
-          // keys that no row sees count as zero, whatever the page holds there
-          if (tail && 64 * pg + row >= n_keys) sbyte = 0;
-          const __half2 s2 = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(sbyte | (sbyte << 8)), __NV_E4M3));
-          e2m1x8_to_half2(word, h[k]);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) h[k][m] = __hmul2(h[k][m], s2);
-        }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint32_t b0l = as_u32(__lows2half2(h[0][m], h[1][m])), b1l = as_u32(__lows2half2(h[2][m], h[3][m]));
-          const uint32_t b0h = as_u32(__highs2half2(h[0][m], h[1][m])), b1h = as_u32(__highs2half2(h[2][m], h[3][m]));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma_f16(o[mt][2 * m], pa[mt], b0l, b1l);
-            mma_f16(o[mt][2 * m + 1], pa[mt], b0h, b1h);
-          }
-        }
-      }
-      if (++stage == L::Stages) {
-        stage = 0;
-        phase ^= 1;
+        for (int r = 0; r < 2; ++r)
+          l_sum[mt][r] = fmaf(p4[mt][2 * r], inv_ts[0], fmaf(p4[mt][2 * r + 1], inv_ts[1], l_sum[mt][r]));
+      if (++qk_stage == L::Stages) {
+        qk_stage = 0;
+        qk_phase ^= 1;
       }
     }
     if (!ok) break;
@@ -458,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if (q == 0) s_l[warp * L::Rows + 16 * mt + 8 * r + g] = l;
       }
-    float4* X = reinterpret_cast<float4*>(smem + L::OffX);
+    float4* X = reinterpret_cast<float4*>(smem + L::OffX);  // (its scores were read before the last barrier)
     if (kh == 1)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
