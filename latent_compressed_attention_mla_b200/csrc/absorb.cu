@@ -533,9 +533,12 @@ cudaError_t launch_absorb_and_plan(const mla_dims& d, const void* q_nope, const 
       return cudaErrorInvalidValue;
     // tokens per CTA: the largest block that still gives every SM a CTA
     const int M = batch * n_q, sms = device_sm_count();
+    // (at most 32 tokens are one block of 32, whose kernel is the narrow one below)
     int tok = 32;
-    if ((long long)d.n_heads * ((M + 127) / 128) >= sms) tok = 128;
-    else if ((long long)d.n_heads * ((M + 63) / 64) >= sms) tok = 64;
+    if (M > 32) {
+      if ((long long)d.n_heads * ((M + 127) / 128) >= sms) tok = 128;
+      else if ((long long)d.n_heads * ((M + 63) / 64) >= sms) tok = 64;
+    }
     // small batches split each head's 512 columns over two CTAs: half the
     // weight fetch per CTA, and two CTAs fit on an SM
     const int nsplit = M <= 32 ? 2 : 1;

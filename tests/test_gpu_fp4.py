@@ -238,3 +238,23 @@ def test_expired_wait_is_reported_and_the_next_step_is_right(heads):
     gp.session.dims = gp.dims
     assert torch.equal(gp.run()[0], ref)
     assert gp.status() == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("heads", [148, 192])
+def test_more_heads_than_multiprocessors(heads, cache):
+    """Few tokens and at least as many heads as multiprocessors: the absorption's
+    32-token kernel, whatever the head count."""
+    cfg = fp4_cfg(n_heads=heads, cache_dtype=cache, B=2, T=1, L=(3, 100))
+    gp = GpuProblem(cfg)
+    out, _ = gp.run()
+    assert gp.status() == 0
+    if cache == "fp4":
+        op = Fp4Oracle(cfg)
+        caches = [op.after(gp, b) for b in range(cfg.B)]
+    else:
+        op = OracleProblem(cfg)
+        caches = [op.cache_values(b) for b in range(cfg.B)]
+    for b in range(cfg.B):
+        o, _ = op.expected_absorbed(b, cache=caches[b])
+        assert rel_err(out[b].double().cpu().numpy(), o) <= 1e-2
