@@ -47,7 +47,10 @@
 //    (at most six significant bits, so exact wherever f16 holds the value's
 //    range).  A staging slot holds 128 columns, enough for two units.  k^R and
 //    q^R stay bf16: TMA brings the k^R unit straight into the ring, and its
-//    MMAs take the bf16 form.
+//    MMAs take the bf16 form.  This variant takes any head count: the rows
+//    (query token, head) of a sequence, r = t * n_heads + h, form groups of 128,
+//    each row with its own causal limit (rows behind the last are computed and
+//    not stored).
 //  * Warp roles: 0-3 softmax + epilogue (one TMEM lane each), 4 TMEM
 //    allocation and (leader) QK issue, 5 (leader) PV issue; bf16 cache: 6-7
 //    TMA for Q and QK data, 8-9 TMA for PV data; FP8 cache: 6 / 7 TMA for
@@ -555,6 +558,7 @@ __device__ __noinline__ void prefetch_first_tile(const DecodeParams& p, int w, i
 
 struct TcParams {
   DecodeParams p;
+  int groups;            // groups of 128 query rows: the query tokens (128 heads each); 4-bit: see below
   CUtensorMap map_q;     // q_abs [rows = batch*n_q*128][576], box 64 x 64 (bf16, or f16 for the FP8 cache)
   CUtensorMap map_o;     // o_part [rows = n_q*n_slots*128][512] fp32, box 32 x 64, 128-byte swizzle
   // bf16 cache
@@ -637,7 +641,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();  // 0 = leader (issues the MMAs)
   const int pair = blockIdx.x >> 1;
-  const int t = pair % p.n_q, w = pair / p.n_q;
+  const int grp = pair % P.groups, w = pair / P.groups;
+  const int n_heads = kFp4 ? p.d.n_heads : kHeads, n_rows = p.n_q * n_heads;  // of a sequence
+  const int row0 = kHeads * grp + kHalfHeads * (int)rank;                     // this CTA's first
+  const int t = kFp4 ? min(n_rows - 1, kHeads * grp + kHeads - 1) / n_heads : grp;  // (last) query token of the group
 
   auto bar = [&](int i) -> uint32_t { return sbase + L::OffBar + 8u * i; };
   auto leader_bar = [&](int i) -> uint32_t { return map_to_rank(bar(i), 0); };
@@ -734,23 +741,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
     // (the first tile of a step executes it from a cold instruction cache).
     const int Lt = warp * 32 + lane;
     const int hl = Lt & 63, half = Lt >> 6;
-    const int head = kHalfHeads * (int)rank + hl;
+    const int row = row0 + hl;                          // this thread's query row,
+    const int row_t = kFp4 ? min(row, n_rows - 1) / n_heads : t;  // its token
+    const bool row_ok = !kFp4 || row < n_rows;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     SegmentWalker walk(p, w, t);
     Segment s;
     uint32_t g = 0;
     bool ok = true;
     while (walk.next(s)) {
-      const size_t slot = (size_t)t * p.n_slots + (w + s.b);
-      // the split partials of this path are bf16 rows (the combine reads them so)
-      __nv_bfloat16* od = reinterpret_cast<__nv_bfloat16*>(p.o_part) + (slot * kHeads + head) * kDC;
+      // the row's place among the split partials, bf16 rows on this path (the combine reads them so)
+      auto part = [&]() -> size_t {
+        if constexpr (!kFp4) return ((size_t)t * p.n_slots + (w + s.b)) * kHeads + kHalfHeads * rank + hl;
+        return ((size_t)row_t * p.n_slots + (w + s.b)) * n_heads + (row - row_t * n_heads);
+      };
       if (s.n_pages == 0 || !ok) {
-        for (int j = 0; j < 2; ++j)
-          for (int c = 0; c < 128; c += 8)
-            *reinterpret_cast<uint4*>(od + 256 * j + 128 * half + c) = make_uint4(0, 0, 0, 0);
-        if (half == 0) p.lse_part[slot * kHeads + head] = -INFINITY;
+        __nv_bfloat16* od = reinterpret_cast<__nv_bfloat16*>(p.o_part) + part() * kDC;
+        if (row_ok) {
+          for (int j = 0; j < 2; ++j)
+            for (int c = 0; c < 128; c += 8)
+              *reinterpret_cast<uint4*>(od + 256 * j + 128 * half + c) = make_uint4(0, 0, 0, 0);
+          if (half == 0) p.lse_part[part()] = -INFINITY;
+        }
         continue;
       }
+      const int row_vis = kFp4 ? p.seq_lens[s.b] - p.n_q + row_t + 1 : s.nvis;  // keys the row sees
       float m_ref = -INFINITY, l_part = 0.f;
       const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
       for (int it = 0; it < n_tiles; ++it, ++g) {
@@ -765,7 +780,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int pg = pg0 + tile_page(2 * half + q);
-          nv[q] = pg < s.page_lo + s.n_pages ? max(0, min(kPage, s.nvis - pg * kPage)) : 0;
+          nv[q] = pg < s.page_lo + s.n_pages ? max(0, min(kPage, row_vis - pg * kPage)) : 0;
         }
         // pass 1: the tile's max (scale > 0 commutes with max)
         float mx = -INFINITY;
@@ -792,6 +807,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
           alpha = fast_exp2(m_ref - tile_max);
           m_ref = tile_max;
         }
+        // a row whose causal limit lies before the group's may not see a key yet
+        const float m_sub = kFp4 && m_ref == -INFINITY ? 0.f : m_ref;
         // pass 2: probabilities of page sub-tile 2*half + q, packed in pairs
         float psum = 0.f;
         auto probs = [&](int q, uint32_t(&pk)[32]) {
@@ -803,8 +820,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const float e0 = fast_exp2(__uint_as_float(sr[2 * j]) * p.scale_log2 - m_ref);
-            const float e1 = fast_exp2(__uint_as_float(sr[2 * j + 1]) * p.scale_log2 - m_ref);
+            const float e0 = fast_exp2(__uint_as_float(sr[2 * j]) * p.scale_log2 - m_sub);
+            const float e1 = fast_exp2(__uint_as_float(sr[2 * j + 1]) * p.scale_log2 - m_sub);
             PT h2;
             if constexpr (kConv) h2 = __floats2half2_rn(e0, e1);
             else h2 = __floats2bfloat162_rn(e0, e1);
@@ -937,7 +954,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
       // staging slots: two iterations of both halves in flight.
       {
         const bool issuer = hl == 0;  // thread 0 of each half
-        const int orow = (int)((((size_t)t * p.n_slots + w + s.b) * kHeads) + kHalfHeads * rank);
+        // (the CTA's rows are one token's where n_heads is a multiple of 64; other
+        // head counts store row by row)
+        const bool boxes = !kFp4 || n_heads % kHalfHeads == 0;
+        const int orow = !kFp4 ? (int)((((size_t)t * p.n_slots + w + s.b) * kHeads) + kHalfHeads * rank)
+                               : (int)(((size_t)(row0 / n_heads) * p.n_slots + w + s.b) * n_heads + row0 % n_heads);
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           const int c = 64 * i;
@@ -960,11 +981,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
                                                               __uint_as_float(orr[8 * q + 2 * e + 1]) * inv);
               u[e] = *reinterpret_cast<const uint32_t*>(&v2);
             }
-            *reinterpret_cast<uint4*>(box + ((q ^ (hl & 7)) * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
+            if (boxes)
+              *reinterpret_cast<uint4*>(box + ((q ^ (hl & 7)) * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
+            else if (kFp4 && row_ok)
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o_part) + part() * kDC + (c < 128 ? 0 : 256) + 128 * half + (c & 127) + 8 * q) =
+                  make_uint4(u[0], u[1], u[2], u[3]);
           }
           fence_proxy_async();
           asm volatile("bar.sync %0, 64;" ::"r"(2 + half) : "memory");
-          if (issuer) {
+          if (issuer && boxes && row_ok) {
             tma_store_2d(&P.map_o, (c < 128 ? 0 : 256) + 128 * half + (c & 127), orow,
                          sbase + L::OffP + ((i & 1) * 2 + half) * 8192);
             bulk_commit();
@@ -975,7 +1000,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
         if (issuer) bulk_wait_all();
         asm volatile("bar.sync %0, 64;" ::"r"(2 + half) : "memory");
       }
-      if (half == 0) p.lse_part[slot * kHeads + head] = l_tot > 0.f ? m_ref + __log2f(l_tot) : -INFINITY;
+      if (half == 0 && row_ok) p.lse_part[part()] = l_tot > 0.f ? m_ref + __log2f(l_tot) : -INFINITY;
       if (threadIdx.x == 0) TC_TRACE(15, 0);
       MLA_STAMP(2);
       tc_fence_before();
@@ -1361,7 +1386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
             // wait only for chunk c
             if (rank == 0)
               for (int c = 0; c < kChunks; ++c) mbar_expect_tx(bar(L::Q_FULL + c), 2 * 8192);
-            const int qrow = ((s.b * p.n_q + t) * kHeads) + kHalfHeads * (int)rank;
+            const int qrow = s.b * n_rows + row0;
             for (int c = 0; c < kChunks; ++c)
               tma_load_2d_pair(sbase + L::OffQ + c * 8192, &P.map_q, 64 * c, qrow, leader_bar(L::Q_FULL + c));
           }
@@ -1766,17 +1791,23 @@ cudaError_t launch_variant(const TcParams& tp, int pairs, cudaStream_t st) {
 }  // namespace
 
 bool decode_tc_supported(const mla_dims& d, int n_q) {
-  return d.n_heads == kHeads && d.d_c == kDC && d.d_rope == kDR && d.page_size == kPage &&
-         d.act_dtype == MLA_BF16 && (d.cache_dtype == MLA_BF16 || is_coded_cache(d)) && n_q >= 1 &&
-         n_q <= 8 && device_is_sm100();
+  if (d.d_c != kDC || d.d_rope != kDR || d.page_size != kPage || d.act_dtype != MLA_BF16 || d.d_v != 128 || n_q < 1 ||
+      !device_is_sm100())
+    return false;
+  // 4-bit: more rows than the few-row kernel takes (its 16 rows cost about 60% of a 128-row group here)
+  if (d.cache_dtype == MLA_FP4_E2M1) return !decode_few_supported(d, n_q) && (long long)n_q * d.n_heads <= 65536;
+  return d.n_heads == kHeads && (d.cache_dtype == MLA_BF16 || d.cache_dtype == MLA_FP8_E4M3) && n_q <= 8;
 }
 
 bool decode_tc_wants_f16_queries(const mla_dims& d) { return is_coded_cache(d); }
 bool decode_tc_wants_bf16_q_rope(const mla_dims& d) { return d.cache_dtype == MLA_FP4_E2M1; }
 
-int decode_tc_auto_splits(int num_sms, int n_q) {
+// groups of 128 query rows
+static int row_groups(const mla_dims& d, int n_q) { return (n_q * d.n_heads + kHeads - 1) / kHeads; }
+
+int decode_tc_auto_splits(const mla_dims& d, int num_sms, int n_q) {
   const int pairs = num_sms / 2;
-  const int w = pairs / (n_q > 0 ? n_q : 1);
+  const int w = pairs / row_groups(d, n_q);
   return w > 0 ? w : 1;
 }
 
@@ -1784,8 +1815,9 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st) {
   TcParams tp;
   memset(&tp, 0, sizeof(tp));
   tp.p = p;
-  const uint64_t q_rows = (uint64_t)p.batch * p.n_q * kHeads;
-  if (!make_o_map(&tp.map_o, p.o_part, (uint64_t)p.n_q * p.n_slots * kHeads)) return cudaErrorInvalidValue;
+  tp.groups = row_groups(p.d, p.n_q);
+  const uint64_t q_rows = (uint64_t)p.batch * p.n_q * p.d.n_heads;
+  if (!make_o_map(&tp.map_o, p.o_part, (uint64_t)p.n_q * p.n_slots * p.d.n_heads)) return cudaErrorInvalidValue;
   if (p.d.cache_dtype == MLA_FP4_E2M1) {
     const Fp4Page f4 = fp4_page(kPage, kDC, kDR);
     tp.scl_off = f4.sc_off;
@@ -1796,7 +1828,7 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st) {
                        p.page_bytes, 64, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
     tp.map_codes_qk = tp.map_codes_pv;
-    return launch_variant<MLA_FP4_E2M1>(tp, p.splits * p.n_q, st);
+    return launch_variant<MLA_FP4_E2M1>(tp, p.splits * tp.groups, st);
   }
   if (p.d.cache_dtype == MLA_FP8_E4M3) {
     const Fp8Page fp = fp8_page(kPage, kDC, kDR);
@@ -1810,13 +1842,13 @@ cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st) {
         !make_page_map(&tp.map_scl, p.pool + fp.sc_off, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, kDC / 128, p.num_pages,
                        p.page_bytes, kDC / 128))
       return cudaErrorInvalidValue;
-    return launch_variant<MLA_FP8_E4M3>(tp, p.splits * p.n_q, st);
+    return launch_variant<MLA_FP8_E4M3>(tp, p.splits * tp.groups, st);
   }
   const uint64_t pool_rows = (uint64_t)p.num_pages * kPage;
   if (!make_map(&tp.map_q, p.q_abs, q_rows, 64) || !make_map(&tp.map_pv, p.pool, pool_rows, 64) ||
       !make_map(&tp.map_pv16, p.pool, pool_rows, 16) || !make_map(&tp.map_row, p.pool, pool_rows, 1))
     return cudaErrorInvalidValue;
-  return launch_variant<MLA_BF16>(tp, p.splits * p.n_q, st);
+  return launch_variant<MLA_BF16>(tp, p.splits * tp.groups, st);
 }
 
 }  // namespace mla

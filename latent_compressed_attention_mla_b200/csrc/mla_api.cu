@@ -77,8 +77,8 @@ int auto_splits(const mla_dims& d, int batch, int n_q) {
   (void)batch;
   const int sms = num_sms();
   if (!(d.flags & MLA_FLAG_FORCE_SIMT)) {
-    if (decode_tc_supported(d, n_q)) return decode_tc_auto_splits(sms, n_q);
-    if (decode_few_supported(d, n_q)) return decode_few_auto_splits(d, sms, n_q);
+    if (decode_tc_supported(d, n_q)) return decode_tc_auto_splits(d, sms, n_q);
+    if (decode_few_supported(d, n_q)) return decode_few_auto_splits(sms);
   }
   const int hg = d.n_heads % 8 == 0 && d.d_c / 16 <= 32 ? 8 : 4;
   const int groups = d.n_heads / hg;  // 0 where no SIMT kernel takes these heads either

@@ -99,8 +99,8 @@ bool make_tile_map_bf16(void* map, const void* base, uint64_t cols, uint64_t row
                         uint32_t box_cols, uint32_t box_rows);
 
 // 3-D map over a sub-block of the cache pages, [pages][rows][row_elems] of bytes
-// or bf16, one page's rows x box_cols per box, 128-byte swizzle (a box row is
-// 128 bytes).
+// or bf16, one page's rows x box_cols per box; a box row is 128 or 32 bytes and
+// the swizzle the one of that width.
 bool make_page_map_swizzled(void* map, const void* base, bool bf16, uint64_t row_elems, uint64_t rows, uint64_t pages,
                             uint64_t page_bytes, uint32_t box_cols);
 
@@ -404,9 +404,9 @@ __device__ __forceinline__ void mla_stamp_now(int e) {
 cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st);
 // few query rows over a 4-bit cache, warp-level tensor cores (decode_few.cu)
 bool decode_few_supported(const mla_dims& d, int n_q);
-int decode_few_auto_splits(const mla_dims& d, int num_sms, int n_q);
+int decode_few_auto_splits(int num_sms);
 cudaError_t launch_decode_few(const DecodeParams& p, cudaStream_t st);
-int decode_tc_auto_splits(int num_sms, int n_q);
+int decode_tc_auto_splits(const mla_dims& d, int num_sms, int n_q);
 
 // part_bf16: the split partials are bf16 rows (the tensor-core decode writes
 // them so), else fp32 (the CUDA-core decode)

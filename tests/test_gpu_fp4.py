@@ -141,27 +141,31 @@ def test_step_rows_append_attend_and_read_together(heads):
 RAGGED = (0, 1, 62, 63, 64, 65, 127, 128, 254, 255, 256, 257, 700, 1500)
 
 
-PATH = {128: 1}  # decode kernel by heads: tcgen05 at 128, warp-level MMA for fewer (2)
+def tc_path(heads, T):
+    """Decode kernel by query rows: warp-level MMA (2) up to 16, tcgen05 (1) above."""
+    return 2 if heads * T <= 16 else 1
 
 
-@pytest.mark.parametrize("heads", [1, 16, 20, 64, 128])
+@pytest.mark.parametrize("heads", [1, 8, 16, 20, 64, 128])
 @pytest.mark.parametrize("T", [1, 2, 3, 8])
 @pytest.mark.parametrize("num_splits", [0, 1, 7])
 def test_tensor_core_ragged(heads, T, num_splits):
-    check(fp4_cfg(n_heads=heads, B=len(RAGGED), T=T, L=RAGGED), num_splits=num_splits, path=PATH.get(heads, 2))
+    check(fp4_cfg(n_heads=heads, B=len(RAGGED), T=T, L=RAGGED), num_splits=num_splits, path=tc_path(heads, T))
 
 
 @pytest.mark.parametrize("heads", [16, 33, 128])
 def test_tensor_core_long(heads):
-    check(fp4_cfg(n_heads=heads, B=1, T=2, L=(9000,)), path=PATH.get(heads, 2))
+    check(fp4_cfg(n_heads=heads, B=1, T=2, L=(9000,)), path=1)
+    check(fp4_cfg(n_heads=heads, B=1, T=1, L=(9000,)), path=tc_path(heads, 1))
 
 
-@pytest.mark.parametrize("heads,T", [(16, 20), (128, 9)])
-def test_many_query_tokens(heads, T):
-    check(fp4_cfg(n_heads=heads, B=2, T=T, L=(30, 200)), path=2)
+@pytest.mark.parametrize("heads,T", [(16, 20), (128, 9), (1, 16), (3, 5), (5, 40), (192, 1), (96, 3)])
+def test_rows_across_query_tokens(heads, T):
+    """Groups of rows that hold several tokens, each with its own causal limit, from empty caches on."""
+    check(fp4_cfg(n_heads=heads, B=3, T=T, L=(0, 63, 200)), path=tc_path(heads, T))
 
 
-@pytest.mark.parametrize("heads", [16, 40, 128])
+@pytest.mark.parametrize("heads", [8, 40, 128])
 def test_rows_behind_the_end_do_not_reach_the_output(heads):
     """Everything past a sequence's last key, in its last page and in pages no
     sequence holds, is NaN (codes, scales, token scales and k^R): the outputs are those
@@ -185,7 +189,7 @@ def test_rows_behind_the_end_do_not_reach_the_output(heads):
     assert gp.status() == 0
 
 
-@pytest.mark.parametrize("heads", [16, 40, 128])
+@pytest.mark.parametrize("heads", [8, 40, 128])
 def test_deterministic_and_page_order_invariant(heads):
     cfg = fp4_cfg(n_heads=heads, B=3, T=2, L=(100, 777, 2000))
     gp = GpuProblem(cfg)
@@ -199,7 +203,7 @@ def test_deterministic_and_page_order_invariant(heads):
     assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
 
 
-@pytest.mark.parametrize("heads", [16, 40, 128])
+@pytest.mark.parametrize("heads", [8, 40, 128])
 def test_bad_pages_and_short_sequences_are_reported(heads):
     cfg = fp4_cfg(n_heads=heads, B=3, T=2, L=(100, 300, 500))
     gp = GpuProblem(cfg)
@@ -224,7 +228,7 @@ def test_bad_pages_and_short_sequences_are_reported(heads):
     assert rel_err(out[2].double().cpu().numpy(), ref[2].double().cpu().numpy()) < 1e-2
 
 
-@pytest.mark.parametrize("heads", [16, 40, 128])
+@pytest.mark.parametrize("heads", [8, 40, 128])
 def test_expired_wait_is_reported_and_the_next_step_is_right(heads):
     """With the self-test flag the load producers issue no load: the bounded waits expire."""
     cfg = fp4_cfg(n_heads=heads, B=2, T=1, L=(100, 300))
