@@ -23,8 +23,8 @@
 // tiles of 128 (two pages):
 //   scores  warp (kg, dq): 32 keys x half of the columns.  The contraction
 //           order is the codes' own (a thread's 32 consecutive codes of a key
-//           are the B fragments of eight k-steps), and the query fragments are
-//           held in registers in that order.  The halves' sums meet in shared memory.
+//           are the B fragments of eight k-steps); the query fragments lie in
+//           shared memory in that order.  The halves' sums meet in shared memory.
 //   softmax warp (kg, dq) finishes 16 keys x all rows; the reference moves only
 //           when a score passes it by 2^8; P goes out as f16
 //   values  warp ds: 64 columns x all keys; a thread takes eight consecutive
@@ -33,9 +33,9 @@
 // Keys of a group of eight are taken in the order n ^ (4 if n is odd), with
 // which both the 16-byte and the 4-byte reads of the 128-byte-swizzled pages
 // (TMA) spread over all banks; the block scales carry the 32-byte swizzle.
-// A tile's softmax, the next tile's scores and its own values follow one
-// another with one barrier in between (scores and P are double-buffered), so
-// that the warps' conversions, MMAs and exchanges overlap.
+// A warp interleaves the scores of tile i + 1 with the values of tile i: two
+// independent streams of conversions and MMAs (two warps a scheduler are too
+// few to hide one stream's latencies; P is double-buffered).
 #include <cuda.h>
 
 #include <cstring>
@@ -63,10 +63,11 @@ constexpr unsigned long long kCopyGraceNs = 200000ull;
 constexpr uint32_t kOffScl = kStages * kStageBytes;                      // [kStages][kTilePages][kSclBytes]
 constexpr uint32_t kOffTs = kOffScl + kStages * kTilePages * kSclBytes;  // [kStages][kTilePages][kTsBytes]
 constexpr uint32_t kXBytes = kWarps * 2 * 512;                           // [kWarps][2][32 lanes] float4
-constexpr uint32_t kOffX = kOffTs + kStages * kTilePages * kTsBytes;     // two of them
+constexpr uint32_t kOffX = kOffTs + kStages * kTilePages * kTsBytes;
 constexpr uint32_t kPBytes = kMaxRows * kTileKeys * 2;                   // [16][128 keys] f16, 16-byte units swizzled
-constexpr uint32_t kOffP = kOffX + 2 * kXBytes;                          // two of them
-constexpr uint32_t kOffMax = kOffP + 2 * kPBytes;                        // int [16]
+constexpr uint32_t kOffP = kOffX + kXBytes;                              // two of them
+constexpr uint32_t kOffQ = kOffP + 2 * kPBytes;                          // [2 halves][kSteps][32 lanes] fragments
+constexpr uint32_t kOffMax = kOffQ + 2 * kSteps * 512;                   // int [16]
 constexpr uint32_t kOffL = kOffMax + kMaxRows * 4;                       // float [kWarps][16]
 constexpr uint32_t kOffBar = kOffL + kWarps * kMaxRows * 4;
 constexpr uint32_t kOffAbort = kOffBar + 2 * kStages * 8;                // barriers: full, then empty, per stage
@@ -110,7 +111,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // Order-preserving map of floats to signed integers (for atomicMax).
 __device__ __forceinline__ int float_order(float x) {
@@ -285,8 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
       // Query fragments.  Step st < 16: contraction indexes 2q, 2q + 1 / 2q + 8,
       // 2q + 9 are columns 256 dq + 128 (st / 8) + 32 q + 4 (st % 8) + {0, 1} /
       // {2, 3}; steps 16, 17: k^R columns 16 q + 8 dq + 4 (st % 2) + {0, 1} / {2, 3} (bf16).
-      uint4 qf[kSteps];
-      {
+      // (The warps of kg 0 write both halves'; read after the barrier below.)
+      const uint4* const qf = reinterpret_cast<const uint4*>(smem + kOffQ) + dq * kSteps * 32 + lane;
+      if (kg == 0) {
+        uint4* const qw = reinterpret_cast<uint4*>(smem + kOffQ) + dq * kSteps * 32 + lane;
         const __half* qa = static_cast<const __half*>(p.q_abs) + ((size_t)s.b * P.rows + g) * kD;
 #pragma unroll
         for (int st = 0; st < kSteps; ++st) {
@@ -294,20 +296,138 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
                                   : kDC + 16 * q + 8 * dq + 4 * (st & 1);
           const uint2 lo = g < P.rows ? *reinterpret_cast<const uint2*>(qa + col) : make_uint2(0, 0);
           const uint2 hi = g + 8 < P.rows ? *reinterpret_cast<const uint2*>(qa + 8 * kD + col) : make_uint2(0, 0);
-          qf[st] = make_uint4(lo.x, hi.x, lo.y, hi.y);
+          qw[32 * st] = make_uint4(lo.x, hi.x, lo.y, hi.y);
         }
       }
+      sync_warps();
       float o[8][4], m_ref[2] = {-INFINITY, -INFINITY}, l_sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      float own[2][4];  // this half's scores of the keys this warp finishes
       const int n_tiles = (s.n_pages + kTilePages - 1) / kTilePages;
       for (int i = -1; i < n_tiles; ++i) {
-        // ---------------------------------------------------- softmax of tile i
+        const bool more = i + 1 < n_tiles;
+        const int key0 = (s.page_lo + (i + 1) * kTilePages) * kPage;  // tile i + 1
+        if (more) {
+          ok = mbar_wait(full(qk_stage), qk_phase, abort_flag) && ok;
+          const int n_keys = nvis_hi - key0;
+          if (n_keys < kTileKeys) {
+            // keys that no row sees count as zero, whatever the page holds there
+            for (int k = tid >> 2; k < kTileKeys; k += 8 * kWarps)
+              if (k >= n_keys) {
+                *reinterpret_cast<uint2*>(smem + kOffScl + qk_stage * kTilePages * kSclBytes + k * 32 + 8 * (tid & 3)) =
+                    make_uint2(0, 0);
+                if ((tid & 3) == 0)
+                  *reinterpret_cast<float*>(smem + kOffTs + qk_stage * kTilePages * kTsBytes + k * 4) = 1.0f;
+              }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a later load overwrites them
+            sync_warps();
+          }
+        }
+        // -------------------------- scores of tile i + 1, values of tile i
+        float acc[4][4];  // scores of four n-tiles of eight keys: two for the other half's warp, then its own
+        const uint8_t* const q_st = smem + qk_stage * kStageBytes;
+        const uint8_t* const q_scl = smem + kOffScl + qk_stage * kTilePages * kSclBytes + qk_scl;
+        const uint32_t* const q_ts =
+            reinterpret_cast<const uint32_t*>(smem + kOffTs + qk_stage * kTilePages * kTsBytes + qk_ts);
+        auto work = [&](auto scores, auto values) {
+          constexpr bool kScores = decltype(scores)::value, kValues = decltype(values)::value;
+          const uint8_t* const v_st = smem + pv_stage * kStageBytes;
+          const uint8_t* const v_scl = smem + kOffScl + pv_stage * kTilePages * kSclBytes;
+          const uint32_t pa_addr = sbase + kOffP + (i & 1) * kPBytes + (lane & 15) * 256;
+          uint4 v[4];
+          uint32_t sc[4][2];
+          if constexpr (kScores) {
+            const uint4 q16 = qf[16 * 32], q17 = qf[17 * 32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int nt = (2 * dq + 2 + j) & 3;
+              const uint4 kr = *reinterpret_cast<const uint4*>(q_st + qk_kr + nt * 1024);
+              // (q^R . k^R) / ts of the accumulator's two keys
+              const float i0 = __uint_as_float(0x7F000000u - q_ts[8 * nt + k0]);
+              const float i1 = __uint_as_float(0x7F000000u - q_ts[8 * nt + k1]);
+              acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+              mma_bf16(acc[j], *reinterpret_cast<const uint32_t(*)[4]>(&q16), kr.x, kr.y);
+              mma_bf16(acc[j], *reinterpret_cast<const uint32_t(*)[4]>(&q17), kr.z, kr.w);
+              acc[j][0] *= i0;
+              acc[j][1] *= i1;
+              acc[j][2] *= i0;
+              acc[j][3] *= i1;
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            if constexpr (kScores) {
+              // columns half t / 4; eight codes of each key: two k-steps
+              if (t % 4 == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int nt = (2 * dq + 2 + j) & 3;
+                  v[j] = *reinterpret_cast<const uint4*>(q_st + (t ? qk_codes1 : qk_codes0) + nt * 1024);
+                  const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(q_scl + nt * 256 + 2 * t));
+                  sc[j][0] = dup_lo(s2);
+                  sc[j][1] = dup_hi(s2);
+                }
+              }
+              const uint4 qa = qf[2 * t * 32], qb = qf[(2 * t + 1) * 32];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t c[4];
+                e2m1x8_to_f16x2(t % 4 == 0 ? v[j].x : t % 4 == 1 ? v[j].y : t % 4 == 2 ? v[j].z : v[j].w, c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[e] = mul_f16x2(c[e], sc[j][(t % 4) >> 1]);
+                mma_f16(acc[j], qa, c[0], c[1]);
+                mma_f16(acc[j], qb, c[2], c[3]);
+              }
+            }
+            if constexpr (kValues) {
+              // columns 64 ds + 8 g .. + 7 of keys 16 t + {k0, k1} and 8 more; the codes of
+              // the two keys are interleaved, so that a byte converts into the f16
+              // pair of one column, and the pair of scales multiplies it
+              const uint32_t kc = (t >> 2) * kCodeBytes + (t & 3) * 2048, ks = (t >> 2) * kSclBytes + (t & 3) * 512;
+              uint4 pa;
+              ldsm_x4(pa_addr + (((2 * t + (lane >> 4)) ^ (lane & 7)) << 4), pa.x, pa.y, pa.z, pa.w);
+              uint32_t b[2][8];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t w0 = *reinterpret_cast<const uint32_t*>(v_st + pv_codes0 + kc + h * 1024);
+                const uint32_t w1 = *reinterpret_cast<const uint32_t*>(v_st + pv_codes1 + kc + h * 1024);
+                const uint32_t s2 =
+                    e4m3x2_to_f16x2(v_scl[pv_scl0 + ks + h * 256] | (uint32_t)v_scl[pv_scl1 + ks + h * 256] << 8);
+                uint32_t he[4], ho[4];  // columns 0, 2, 4, 6 and 1, 3, 5, 7
+                e2m1x8_to_f16x2((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), he);
+                e2m1x8_to_f16x2(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), ho);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                  b[h][2 * m] = mul_f16x2(he[m], s2);
+                  b[h][2 * m + 1] = mul_f16x2(ho[m], s2);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) mma_f16(o[j], pa, b[0][j], b[1][j]);
+            }
+          }
+        };
+        using Yes = std::true_type;
+        using No = std::false_type;
+        if (i < 0) work(Yes(), No());
+        else if (more) work(Yes(), Yes());
+        else work(No(), Yes());
+        if (i >= 0) {
+          __syncwarp();  // every lane has read tile i
+          if (lane == 0) mbar_arrive(empty(pv_stage));
+          pv_stage = pv_stage + 1 == kStages ? 0 : pv_stage + 1;
+        }
+        if (!more) break;
+        // the other half's sums of the keys this warp finishes
+        float4* const X = reinterpret_cast<float4*>(smem + kOffX) + lane;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) X[warp * 64 + 32 * j] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+        asm volatile("bar.sync %0, 64;" ::"r"(2 + kg) : "memory");  // the two halves of key group kg
+        // ------------------------------------------------ softmax of tile i + 1
         // keys 32 kg + 16 dq + 8 h + {k0, k1}; rows g, g + 8
         float x[2][4], p4[2][4], inv_ts[2][2];
         bool over = false;  // a score passes its row's reference by more than the threshold
-        uint8_t* const Pb = smem + kOffP + (i & 1) * kPBytes;
+        uint8_t* const Pb = smem + kOffP + ((i + 1) & 1) * kPBytes;
         auto probabilities = [&]() {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -321,114 +441,39 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
             }
           }
         };
-        if (i >= 0) {
-          // the other half's sums of these keys
-          const float4* X = reinterpret_cast<const float4*>(smem + kOffX + (i & 1) * kXBytes) + (warp ^ 1) * 64 + lane;
-          const uint32_t* ts =
-              reinterpret_cast<const uint32_t*>(smem + kOffTs + pv_stage * kTilePages * kTsBytes + qk_ts) + 16 * dq;
-          const int key0 = (s.page_lo + i * kTilePages) * kPage;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 y = X[32 * h];
-            const float f[4] = {own[h][0] + y.x, own[h][1] + y.y, own[h][2] + y.z, own[h][3] + y.w};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t u = ts[8 * h + (c ? k1 : k0)];
-              const float a = __uint_as_float(u) * p.scale_log2, e = (float)((int)(u >> 23) - 127);
-              inv_ts[h][c] = __uint_as_float(0x7F000000u - u);
-              x[h][c] = fmaf(f[c], a, e);
-              x[h][2 + c] = fmaf(f[2 + c], a, e);
-            }
-          }
-          if (key0 + kTileKeys > nvis_lo) {  // some key of the tile is hidden from some row
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int row = min(g + 8 * (c >> 1), P.rows - 1);  // t * n_heads + h
-              const int nvis = min(s.len - p.n_q + row / p.d.n_heads + 1, s.end);
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (key0 + 32 * kg + 16 * dq + 8 * h + ((c & 1) ? k1 : k0) >= nvis) x[h][c] = -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) over |= x[h][c] > m_ref[c >> 1] + kRescaleThreshold;
-          probabilities();
-        }
-        // ------------------------------------------------- scores of tile i + 1
-        if (i + 1 < n_tiles) {
-          const uint8_t* st = smem + qk_stage * kStageBytes;
-          uint8_t* scl = smem + kOffScl + qk_stage * kTilePages * kSclBytes;
-          uint8_t* tsb = smem + kOffTs + qk_stage * kTilePages * kTsBytes;
-          float4* X = reinterpret_cast<float4*>(smem + kOffX + ((i + 1) & 1) * kXBytes);
-          ok = mbar_wait(full(qk_stage), qk_phase, abort_flag) && ok;
-          const int n_keys = nvis_hi - (s.page_lo + (i + 1) * kTilePages) * kPage;
-          if (n_keys < kTileKeys) {
-            // keys that no row sees count as zero, whatever the page holds there
-            for (int k = tid >> 2; k < kTileKeys; k += 8 * kWarps)
-              if (k >= n_keys) {
-                *reinterpret_cast<uint2*>(scl + k * 32 + 8 * (tid & 3)) = make_uint2(0, 0);
-                if ((tid & 3) == 0) *reinterpret_cast<float*>(tsb + k * 4) = 1.0f;
-              }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a later load overwrites them
-            sync_warps();
-          }
-          // four n-tiles of eight keys: two for the other half's warp, then its own
-          float acc[4][4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int nt = (2 * dq + 2 + j) & 3;
-            const uint4 kr = *reinterpret_cast<const uint4*>(st + qk_kr + nt * 1024);
-            // (q^R . k^R) / ts of the accumulator's two keys
-            const uint32_t* ts = reinterpret_cast<const uint32_t*>(tsb + qk_ts) + 8 * nt;
-            const float i0 = __uint_as_float(0x7F000000u - ts[k0]), i1 = __uint_as_float(0x7F000000u - ts[k1]);
-            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-            mma_bf16(acc[j], *reinterpret_cast<const uint32_t(*)[4]>(&qf[16]), kr.x, kr.y);
-            mma_bf16(acc[j], *reinterpret_cast<const uint32_t(*)[4]>(&qf[17]), kr.z, kr.w);
-            acc[j][0] *= i0;
-            acc[j][1] *= i1;
-            acc[j][2] *= i0;
-            acc[j][3] *= i1;
-          }
+        for (int h = 0; h < 2; ++h) {
+          const float4 y = X[(warp ^ 1) * 64 + 32 * h];
+          const float f[4] = {acc[2 + h][0] + y.x, acc[2 + h][1] + y.y, acc[2 + h][2] + y.z, acc[2 + h][3] + y.w};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint4 v[4];
-            __half2 sc[4][2];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int nt = (2 * dq + 2 + j) & 3;
-              v[j] = *reinterpret_cast<const uint4*>(st + (c ? qk_codes1 : qk_codes0) + nt * 1024);
-              const __half2 s2 = __half2(__nv_cvt_fp8x2_to_halfraw2(
-                  *reinterpret_cast<const uint16_t*>(scl + qk_scl + nt * 256 + 8 * c), __NV_E4M3));
-              sc[j][0] = __low2half2(s2);
-              sc[j][1] = __high2half2(s2);
-            }
-#pragma unroll
-            for (int wi = 0; wi < 4; ++wi)  // eight codes of each key: two k-steps
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                __half2 hc[4];
-                e2m1x8_to_half2(wi == 0 ? v[j].x : wi == 1 ? v[j].y : wi == 2 ? v[j].z : v[j].w, hc);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) hc[e] = __hmul2(hc[e], sc[j][wi >> 1]);
-                mma_f16(acc[j], qf[8 * c + 2 * wi], as_u32(hc[0]), as_u32(hc[1]));
-                mma_f16(acc[j], qf[8 * c + 2 * wi + 1], as_u32(hc[2]), as_u32(hc[3]));
-              }
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            X[warp * 64 + 32 * j + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) own[j][c] = acc[2 + j][c];
-          }
-          if (++qk_stage == kStages) {
-            qk_stage = 0;
-            qk_phase ^= 1;
+            const uint32_t u = q_ts[16 * dq + 8 * h + (c ? k1 : k0)];
+            const float a = __uint_as_float(u) * p.scale_log2, e = (float)((int)(u >> 23) - 127);
+            inv_ts[h][c] = __uint_as_float(0x7F000000u - u);
+            x[h][c] = fmaf(f[c], a, e);
+            x[h][2 + c] = fmaf(f[2 + c], a, e);
           }
         }
-        // P of tile i and the scores of i + 1 are published; every warp is done
-        // with tile i - 1
+        if (key0 + kTileKeys > nvis_lo) {  // some key of the tile is hidden from some row
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int row = min(g + 8 * (c >> 1), P.rows - 1);  // t * n_heads + h
+            const int nvis = min(s.len - p.n_q + row / p.d.n_heads + 1, s.end);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (key0 + 32 * kg + 16 * dq + 8 * h + ((c & 1) ? k1 : k0) >= nvis) x[h][c] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) over |= x[h][c] > m_ref[c >> 1] + kRescaleThreshold;
+        probabilities();
+        if (++qk_stage == kStages) {
+          qk_stage = 0;
+          qk_phase ^= 1;
+        }
+        // P of tile i + 1 is published
         if (sync_warps_or(over || !ok)) {
           ok = !sync_warps_or(!ok);
           if (!ok) break;
@@ -459,46 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
           sync_warps();
           if (tid < kMaxRows) s_max[tid] = float_order(-INFINITY);
         }
-        if (i < 0) continue;
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             l_sum[r] = fmaf(p4[h][2 * r], inv_ts[h][0], fmaf(p4[h][2 * r + 1], inv_ts[h][1], l_sum[r]));
-        // ----------------------------------------------------- values of tile i
-        // thread: columns 64 ds + 8 g .. + 7 of keys 16 kb + {k0, k1} and 8 more; the
-        // codes of the two keys are interleaved, so that a byte converts into
-        // the f16 pair of one column, and the pair of scales multiplies it
-        const uint8_t* st = smem + pv_stage * kStageBytes;
-        const uint8_t* scl = smem + kOffScl + pv_stage * kTilePages * kSclBytes;
-        const uint32_t pa_addr = smem_addr(Pb) + (lane & 15) * 256;
-#pragma unroll
-        for (int kb = 0; kb < 8; ++kb) {
-          const uint32_t kc = (kb >> 2) * kCodeBytes + (kb & 3) * 2048, ks = (kb >> 2) * kSclBytes + (kb & 3) * 512;
-          uint4 pa;
-          ldsm_x4(pa_addr + (((2 * kb + (lane >> 4)) ^ (lane & 7)) << 4), pa.x, pa.y, pa.z, pa.w);
-          uint32_t b[2][8];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // keys 16 kb + 8 h + {k0, k1}
-            const uint32_t w0 = *reinterpret_cast<const uint32_t*>(st + pv_codes0 + kc + h * 1024);
-            const uint32_t w1 = *reinterpret_cast<const uint32_t*>(st + pv_codes1 + kc + h * 1024);
-            const uint32_t s0 = scl[pv_scl0 + ks + h * 256], s1 = scl[pv_scl1 + ks + h * 256];
-            const __half2 s2 = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(s0 | (s1 << 8)), __NV_E4M3));
-            __half2 he[4], ho[4];  // columns 0, 2, 4, 6 and 1, 3, 5, 7
-            e2m1x8_to_half2((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), he);
-            e2m1x8_to_half2(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), ho);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              b[h][2 * m] = as_u32(__hmul2(he[m], s2));
-              b[h][2 * m + 1] = as_u32(__hmul2(ho[m], s2));
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) mma_f16(o[j], pa, b[0][j], b[1][j]);
-        }
-        __syncwarp();  // every lane has read the tile
-        if (lane == 0) mbar_arrive(empty(pv_stage));
-        pv_stage = pv_stage + 1 == kStages ? 0 : pv_stage + 1;
       }
       if (!ok) break;
       // ------------------------------------------------------------- epilogue

@@ -433,30 +433,26 @@ __device__ __forceinline__ void e4m3x4_scaled(uint32_t w, __half2 s2, uint32_t& 
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// Scales of 32 columns (two blocks) as f16 pairs: e4m3 block scales (low byte
-// first) times the token's scale.
-__device__ __forceinline__ void fp4_block_scales(uint32_t sc, __half2 ts, __half2& s0, __half2& s1) {
-  const __half2 s = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)sc, __NV_E4M3)), ts);
-  s0 = __low2half2(s);
-  s1 = __high2half2(s);
-}
-
 // 32 e2m1 codes (two blocks of 16 columns) times their scales -> 64 bytes of
-// f16: the 16-byte units u0 ^ e, e = 0..3, of a 128-byte swizzled row.
-__device__ __forceinline__ void store_e2m1x32(uint8_t* row, uint32_t u0, const uint4& w, __half2 s0, __half2 s1) {
+// f16: the 16-byte units u0 ^ e, e = 0..3, of a 128-byte swizzled row.  sc: the
+// blocks' e4m3 scales (low byte first); ts: the token's scale, twice.
+__device__ __forceinline__ void store_e2m1x32(uint8_t* row, uint32_t u0, const uint4& w, uint32_t sc, uint32_t ts) {
   const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+  const uint32_t s = mul_f16x2(e4m3x2_to_f16x2(sc), ts), s0 = dup_lo(s), s1 = dup_hi(s);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    __half2 h[4];
-    e2m1x8_to_half2(words[i], h);
     uint32_t r[4];
+    e2m1x8_to_f16x2(words[i], r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __half2 v = __hmul2(h[e], i < 2 ? s0 : s1);
-      r[e] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+    for (int e = 0; e < 4; ++e) r[e] = mul_f16x2(r[e], i < 2 ? s0 : s1);
     *reinterpret_cast<uint4*>(row + ((u0 ^ i) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
   }
+}
+
+// A float as an f16 pair of twice its value.
+__device__ __forceinline__ uint32_t f16x2_of(float x) {
+  const __half2 h = __float2half2_rn(x);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Two bf16 (one 32-bit word) -> two f16 (round to nearest).
@@ -1074,11 +1070,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
             const uint8_t* const sclr = scl + row * 32 + (pv ? 8 * (int)rank : 8 * c);
             const uint8_t* const tsr = scl + 2048 + row * 4;
             uint2 g0 = *reinterpret_cast<const uint2*>(sclr), g1 = *reinterpret_cast<const uint2*>(sclr + scl_g);
-            __half2 ts[2] = {__float2half2_rn(*reinterpret_cast<const float*>(tsr)),
-                             __float2half2_rn(*reinterpret_cast<const float*>(tsr + ts_a))};
+            uint32_t ts[2] = {f16x2_of(*reinterpret_cast<const float*>(tsr)),
+                              f16x2_of(*reinterpret_cast<const float*>(tsr + ts_a))};
             if (!live) {  // zero scales: the codes of rows past the end may be anything
               g0 = g1 = make_uint2(0, 0);
-              ts[0] = ts[1] = __float2half2_rn(0.f);
+              ts[0] = ts[1] = 0;
             }
             const uint32_t m01 = pv ? g0.y : g1.x, m10 = pv ? g1.x : g0.y;  // (unit, half)
 #pragma unroll 1
@@ -1091,11 +1087,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
               if (!ok) break;
               uint8_t* const dst = ring + unit.slot * kUnitBytes;
 #pragma unroll
-              for (int a = 0; a < 2; ++a) {
-                __half2 s0, s1;
-                fp4_block_scales((sc[a] >> (16 * q)) & 0xFFFFu, ts[a], s0, s1);
-                store_e2m1x32(dst + a * 8192, u0, v[a], s0, s1);
-              }
+              for (int a = 0; a < 2; ++a) store_e2m1x32(dst + a * 8192, u0, v[a], sc[a] >> (16 * q), ts[a]);
               fence_proxy_async();
               __syncwarp();
               if (lane == 0) mbar_arrive_cluster(un_full + 8 * unit.slot);

@@ -180,8 +180,7 @@ __device__ __forceinline__ float finite_abs(float v, bool& finite) {
 // (The bytes are taken apart inside the asm block: the conversion reads them
 // in place.  cuda_fp4.h's one-byte conversions cost an extraction each:
 // measured 47 against 96 codes per cycle and SM with 16 warps.)
-__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, __half2 (&h)[4]) {
-  uint32_t r[4];
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
@@ -190,9 +189,22 @@ __device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, __half2 (&h)[4]) {
       "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
       : "r"(w));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __half2*>(&r[i]);
 }
+// f16 pairs held as 32-bit words
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// two e4m3 codes (low byte first) as an f16 pair
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t s) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(s));
+  return d;
+}
+__device__ __forceinline__ uint32_t dup_lo(uint32_t h) { return __byte_perm(h, h, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t h) { return __byte_perm(h, h, 0x3232); }
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
 
 // RoPE frequency of rotation pair i of a d_rope-wide vector: base^(-i/half),
 // in double precision.

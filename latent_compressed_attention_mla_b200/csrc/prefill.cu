@@ -111,13 +111,13 @@ __device__ __forceinline__ void gather_row(const PrefillArgs& a, int b, int S, i
     const uint2 w = reinterpret_cast<const uint2*>(pg + (size_t)row * (kPDc / 2))[lane];
     const float scale = e4m3_to_float(pg[f4.sc_off + (size_t)row * (kPDc / 16) + lane]) *
                         reinterpret_cast<const float*>(pg + f4.ts_off)[row];
-    __half2 h[8];
-    e2m1x8_to_half2(w.x, *reinterpret_cast<__half2(*)[4]>(&h[0]));
-    e2m1x8_to_half2(w.y, *reinterpret_cast<__half2(*)[4]>(&h[4]));
+    uint32_t h[8];
+    e2m1x8_to_f16x2(w.x, *reinterpret_cast<uint32_t(*)[4]>(&h[0]));
+    e2m1x8_to_f16x2(w.y, *reinterpret_cast<uint32_t(*)[4]>(&h[4]));
     uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 f = __half22float2(h[i]);
+      const float2 f = f16x2_to_float2(h[i]);
       const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * scale, f.y * scale);
       o[i] = *reinterpret_cast<const uint32_t*>(&v);
     }

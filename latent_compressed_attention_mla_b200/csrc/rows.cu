@@ -350,12 +350,12 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const __grid_consta
           const uint2 w = *reinterpret_cast<const uint2*>(pg + (size_t)prow * (a.d_c / 2) + 8 * b);
           const float s = e4m3_to_float(pg[f4.sc_off + (size_t)prow * (a.d_c / 16) + b]) *
                           reinterpret_cast<const float*>(pg + f4.ts_off)[prow];
-          __half2 h[8];
-          e2m1x8_to_half2(w.x, *reinterpret_cast<__half2(*)[4]>(&h[0]));
-          e2m1x8_to_half2(w.y, *reinterpret_cast<__half2(*)[4]>(&h[4]));
+          uint32_t h[8];
+          e2m1x8_to_f16x2(w.x, *reinterpret_cast<uint32_t(*)[4]>(&h[0]));
+          e2m1x8_to_f16x2(w.y, *reinterpret_cast<uint32_t(*)[4]>(&h[4]));
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 f = __half22float2(h[e]);
+            const float2 f = f16x2_to_float2(h[e]);
             x[2 * e] = f.x * s;
             x[2 * e + 1] = f.y * s;
           }
