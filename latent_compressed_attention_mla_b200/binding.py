@@ -24,6 +24,8 @@ ERRORS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "M
           4: "MLA_ERR_ALIGNMENT", 5: "MLA_ERR_LAUNCH", 6: "MLA_ERR_TIMEOUT", 7: "MLA_ERR_BOUNDS",
           8: "MLA_ERR_CUDA"}
 
+DTYPES = {"f32": MLA_F32, "bf16": MLA_BF16, "fp8": MLA_FP8_E4M3, "fp4": MLA_FP4_E2M1}
+
 # Every entry point declared in include/mla.h.
 EXPORTED = ("mla_cache_page_bytes", "mla_check_dims", "mla_append_workspace_bytes",
             "mla_append_workspace_bytes_fast", "mla_append_latent",
@@ -95,7 +97,7 @@ def error_string(code: int) -> str:
 
 def make_dims(n_heads, d_c, d_rope, d_nope, d_v, d_model, page_size=64, act="bf16", cache="bf16",
               softmax_scale=None, rope_base=10000.0, flags=0) -> MlaDims:
-    codes = {"f32": MLA_F32, "bf16": MLA_BF16, "fp8": MLA_FP8_E4M3, "fp4": MLA_FP4_E2M1}
+    codes = DTYPES
     if softmax_scale is None:
         softmax_scale = (d_nope + d_rope) ** -0.5
     return MlaDims(n_heads, d_c, d_rope, d_nope, d_v, d_model, page_size, codes[act], codes[cache],
@@ -108,14 +110,16 @@ def dims_for(cfg, flags: int = 0) -> MlaDims:
                      cfg.act_dtype, cfg.cache_dtype, cfg.softmax_scale, cfg.rope_base, flags)
 
 
+# (Plain integers pass as c_void_p arguments; making a c_void_p, or a
+# torch.cuda.Stream object for the current stream, costs microseconds a call.)
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(rc: int, what: str):
@@ -182,11 +186,14 @@ def mla_append_latent_noalloc(dims, h, seq_idx, pos, W_dkv, W_kr, page_table, ca
     _check(rc, "mla_append_latent_noalloc")
 
 
-def _rows(x, width, what):
-    """Row stride (elements) of a [N, width] CUDA tensor with contiguous rows."""
-    if x.dim() != 2 or x.shape[1] != width or not x.is_cuda or (width > 1 and x.shape[0] > 0 and x.stride(1) != 1):
-        raise ValueError(f"{what}: a CUDA tensor [N, {width}] with contiguous rows")
-    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), width)
+def _rows(x, n, width, dtype, what):
+    """Row stride (elements) of an [n, width] CUDA tensor with contiguous rows."""
+    if tuple(x.shape) != (n, width) or x.dtype != dtype or not x.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor [{n}, {width}] of {dtype}")
+    step, unit = x.stride()
+    if unit != 1 and width > 1 and n > 0:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return step if n > 1 else max(step, width)
 
 
 def _index(n, *ts):
@@ -207,12 +214,9 @@ def mla_append_rows(dims, c, k_rope, seq_idx, pos, page_table, cache_pool, norm_
     (seq_idx[n], pos[n]) of the paged cache."""
     _cuda(seq_idx, pos, page_table, cache_pool, norm_weight)
     n, act = c.shape[0], act_dtype(dims)
-    cs, ks = _rows(c, dims.d_c, "c"), _rows(k_rope, dims.d_rope, "k_rope")
-    if k_rope.shape[0] != n:
-        raise ValueError("c and k_rope: the same number of rows")
-    if c.dtype != act or k_rope.dtype != act or (norm_weight is not None and
-                                                 (norm_weight.dtype != act or norm_weight.numel() != dims.d_c)):
-        raise ValueError(f"c, k_rope and norm_weight [d_c]: {act}")
+    cs, ks = _rows(c, n, dims.d_c, act, "c"), _rows(k_rope, n, dims.d_rope, act, "k_rope")
+    if norm_weight is not None and (norm_weight.dtype != act or norm_weight.numel() != dims.d_c):
+        raise ValueError(f"norm_weight: [d_c] of {act}")
     _index(n, seq_idx, pos)
     num_pages = cache_pool.numel() * cache_pool.element_size() // cache_page_bytes(dims)
     rc = lib().mla_append_rows(ctypes.byref(dims), _ptr(c), cs, _ptr(k_rope), ks, _ptr(norm_weight), norm_eps, n,

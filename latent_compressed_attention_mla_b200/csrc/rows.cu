@@ -461,8 +461,8 @@ extern "C" int mla_append_rows(const mla_dims* dims, const void* c, int64_t c_st
   a.status = device_status_word();
   a.timeline = timeline_ptr();
   const int half = dims->d_rope / 2;
-  for (int i = 0; i < half && i < kMaxHalf; ++i)
-    a.inv_freq[i] = exp(-log((double)dims->rope_base) * (double)i / (double)half);
+  const double log_base = log((double)dims->rope_base);
+  for (int i = 0; i < half && i < kMaxHalf; ++i) a.inv_freq[i] = exp(-log_base * (double)i / (double)half);
   const size_t es = dims->act_dtype == MLA_F32 ? 4 : 2, cs = dims->cache_dtype == MLA_F32 ? 4 : 2;
   bool vec = aligned16(c) && (size_t)c_stride * es % 16 == 0 && aligned16(norm_weight);
   // unquantised rows lie d_c + d_rope elements apart
