@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(288) append_splitk_finish_kernel(const AppendA
       } else if (CACHE == MLA_FP4_E2M1) {
         const Fp4Page f4 = fp4_page(a.page_size, 512, 64);
         const uint32_t sc = fp4_block_scale(amax16, ts, finite);
-        pg[(size_t)prow * 256 + tid] = (uint8_t)fp4_pair(x0, x1, e4m3_to_float((uint8_t)sc) * ts);
+        const float step = e4m3_to_float((uint8_t)sc) * ts, inv = fp4_inverse(step);
+        pg[(size_t)prow * 256 + tid] = inv > 0.f ? (uint8_t)fp4_pair(x0, x1, step, inv) : (uint8_t)0;
         if ((tid & 7) == 0) pg[f4.sc_off + (size_t)prow * 32 + (tid >> 3)] = (uint8_t)sc;
         if (tid == 0) reinterpret_cast<float*>(pg + f4.ts_off)[prow] = ts;
       } else {

@@ -163,11 +163,20 @@ __device__ __forceinline__ uint32_t fp4_block_scale(float amax, float ts, bool f
   if (!finite) return kE4M3NaN;
   return (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f * ts), __NV_SATFINITE, __NV_E4M3);
 }
-// codes of two elements, the first in the low half; step = block scale * ts
-__device__ __forceinline__ uint32_t fp4_pair(float v0, float v1, float step) {
-  if (!(step > 0.f)) return 0u;
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(__fdiv_rn(v0, step), __fdiv_rn(v1, step)), __NV_E2M1,
-                                            cudaRoundNearest);
+// codes of two elements, the first in the low half; step = block scale * ts,
+// inv its correctly rounded reciprocal (0 where step is 0 or NaN: code 0).  The
+// quotient is v * inv and one correction by its residual, which is within 2^-44
+// of v / step before its last rounding.  That gives the code of the correctly
+// rounded quotient: codes change only at m = .25, .75, 1.25, 1.75, 2.5, 3.5 and
+// 5.  step has four significant bits, so m step is a float; where v equals it,
+// the correction ends on m, and elsewhere v / step is away from m by v's last
+// place at least, 2^-23 / 1.97 of m, more than half of the quotient's last place
+// (2^-24).  Steps lie in [2^-109, 2^126], so near a border nothing underflows.
+__device__ __forceinline__ float fp4_inverse(float step) { return step > 0.f ? __frcp_rn(step) : 0.f; }
+__device__ __forceinline__ uint32_t fp4_pair(float v0, float v1, float step, float inv) {
+  const float q0 = v0 * inv, q1 = v1 * inv;
+  const float c0 = fmaf(fmaf(-q0, step, v0), inv, q0), c1 = fmaf(fmaf(-q1, step, v1), inv, q1);
+  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(c0, c1), __NV_E2M1, cudaRoundNearest);
 }
 // |v| for the maxima: non-finite elements count as 0 and clear `finite`
 __device__ __forceinline__ float finite_abs(float v, bool& finite) {

@@ -44,7 +44,7 @@ struct RowsArgs {
   uint8_t* pool;
   int num_pages;
   size_t page_bytes;
-  int d_c, d_rope, page_size;
+  int d_c, d_rope, page_size, page_shift;  // page_shift: log2 of page_size, or -1
   float rope_base;
   int* status;
   unsigned long long* timeline;
@@ -55,9 +55,10 @@ struct RowsArgs {
 template <typename A>
 __device__ __forceinline__ int row_slot(const A& a, int n, int lane, int* row, int* position) {
   const int b = a.seq_idx[n], p = a.pos[n];
-  const bool ok = b >= 0 && b < a.batch && p >= 0 && p / a.page_size < a.max_pages;
-  const int page = ok ? a.page_table[(size_t)b * a.max_pages + p / a.page_size] : -1;
-  *row = p % a.page_size;
+  const int lp = a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
+  const bool ok = b >= 0 && b < a.batch && p >= 0 && lp < a.max_pages;
+  const int page = ok ? a.page_table[(size_t)b * a.max_pages + lp] : -1;
+  *row = p - lp * a.page_size;
   *position = p;
   if (page < 0 || page >= a.num_pages) {
     if (lane == 0) record_status(a.status, MLA_ERR_BOUNDS);
@@ -163,11 +164,20 @@ __device__ __forceinline__ void store_fp4(uint8_t* pg, const Fp4Page& f4, int pr
   bool finite[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    amax[j] = 0.f;
-    finite[j] = true;
+    float m = 0.f, z = 0.f;  // z: 0 unless an element is not finite
 #pragma unroll
-    for (int e = 0; e < 16; ++e) amax[j] = fmaxf(amax[j], finite_abs(x[j][e], finite[j]));
-    c_max = fmaxf(c_max, amax[j]);
+    for (int e = 0; e < 16; ++e) {
+      m = fmaxf(m, fabsf(x[j][e]));
+      z = fmaf(x[j][e], 0.f, z);
+    }
+    finite[j] = z == 0.f;
+    if (!finite[j]) {
+      m = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) m = fmaxf(m, finite_abs(x[j][e], finite[j]));
+    }
+    amax[j] = m;
+    c_max = fmaxf(c_max, m);
   }
   const float ts = fp4_token_scale(warp_max(c_max), kr_max);
 #pragma unroll
@@ -176,9 +186,12 @@ __device__ __forceinline__ void store_fp4(uint8_t* pg, const Fp4Page& f4, int pr
     if (b < nb) {
       const uint32_t sc = fp4_block_scale(amax[j], ts, finite[j]);
       const float step = e4m3_to_float((uint8_t)sc) * ts;
+      const float inv = fp4_inverse(step);
       uint32_t w[2] = {0u, 0u};
+      if (inv > 0.f) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e >> 2] |= fp4_pair(x[j][2 * e], x[j][2 * e + 1], step) << (8 * (e & 3));
+        for (int e = 0; e < 8; ++e) w[e >> 2] |= fp4_pair(x[j][2 * e], x[j][2 * e + 1], step, inv) << (8 * (e & 3));
+      }
       *reinterpret_cast<uint2*>(pg + (size_t)prow * (d_c / 2) + 8 * b) = make_uint2(w[0], w[1]);
       pg[f4.sc_off + (size_t)prow * (d_c / 16) + b] = (uint8_t)sc;
     }
@@ -315,7 +328,7 @@ struct ReadArgs {
   int batch, max_pages;
   const int32_t* seq_idx;
   const int32_t* pos;
-  int n_tokens, d_c, d_rope, page_size;
+  int n_tokens, d_c, d_rope, page_size, page_shift;
   void* c_out;   // [n][d_c]
   void* kr_out;  // [n][d_rope]
   int* status;
@@ -377,10 +390,17 @@ __global__ void __launch_bounds__(kThreads) read_rows_kernel(const __grid_consta
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// One warp per token up to four CTAs per SM, then every warp loops.
+// One warp per token, up to 32 CTAs per SM, then every warp loops.
 int rows_grid(int n_tokens) {
-  const int ctas = (n_tokens + kWarps - 1) / kWarps, most = 4 * device_sm_count();
+  const int ctas = (n_tokens + kWarps - 1) / kWarps, most = 32 * device_sm_count();
   return ctas < most ? ctas : most;
+}
+
+// log2 of a page size that is a power of two, else -1.
+int page_shift(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size && s < 30) ++s;
+  return (1 << s) == page_size ? s : -1;
 }
 
 template <typename T, int CACHE>
@@ -416,6 +436,7 @@ cudaError_t launch_append_fp4_finalize(const mla_dims& d, const float* raw, int 
   a.d_c = d.d_c;
   a.d_rope = d.d_rope;
   a.page_size = d.page_size;
+  a.page_shift = page_shift(d.page_size);
   a.status = status;
   a.timeline = timeline_ptr();
   auto kernel = d.d_c <= 512 ? append_fp4_finalize_kernel<1> : append_fp4_finalize_kernel<2>;
@@ -457,6 +478,7 @@ extern "C" int mla_append_rows(const mla_dims* dims, const void* c, int64_t c_st
   a.d_c = dims->d_c;
   a.d_rope = dims->d_rope;
   a.page_size = dims->page_size;
+  a.page_shift = page_shift(dims->page_size);
   a.rope_base = dims->rope_base;
   a.status = device_status_word();
   a.timeline = timeline_ptr();
@@ -515,6 +537,7 @@ extern "C" int mla_read_rows(const mla_dims* dims, const void* cache_pool, int n
   a.d_c = dims->d_c;
   a.d_rope = dims->d_rope;
   a.page_size = dims->page_size;
+  a.page_shift = page_shift(dims->page_size);
   a.c_out = c_out;
   a.kr_out = k_out;
   a.status = device_status_word();
