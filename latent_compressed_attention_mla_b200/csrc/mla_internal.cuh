@@ -160,8 +160,14 @@ __device__ __forceinline__ float fp4_token_scale(float amax_c, float amax_kr) {
   return a > 0.f ? __uint_as_float((uint32_t)(k + 127) << 23) : 1.0f;
 }
 __device__ __forceinline__ uint32_t fp4_block_scale(float amax, float ts, bool finite) {
-  if (!finite) return kE4M3NaN;
-  return (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f * ts), __NV_SATFINITE, __NV_E4M3);
+  // amax / (6 ts): the power of two first, exactly, then the sixth with one
+  // residual correction (the code is that of the correctly rounded quotient, as
+  // at fp4_pair: an e4m3 border has five significant bits, six times it seven)
+  const float z = amax * __uint_as_float((254u << 23) - __float_as_uint(ts));
+  const float q = z * (1.0f / 6.0f);
+  const uint32_t code = (uint32_t)__nv_cvt_float_to_fp8(fmaf(fmaf(-6.0f, q, z), 1.0f / 6.0f, q), __NV_SATFINITE,
+                                                        __NV_E4M3);
+  return finite ? code : kE4M3NaN;
 }
 // codes of two elements, the first in the low half; step = block scale * ts,
 // inv its correctly rounded reciprocal (0 where step is 0 or NaN: code 0).  The

@@ -35,7 +35,7 @@ struct RowsArgs {
   const void* kr;      // [n][kr_stride]
   long long kr_stride;
   const void* norm_w;  // [d_c] or null
-  double norm_eps;
+  double norm_eps, inv_dc;
   int n_tokens;
   const int32_t* seq_idx;
   const int32_t* pos;
@@ -53,15 +53,13 @@ struct RowsArgs {
 
 // Physical (page, row) of token n, or page -1 (recorded) if out of range.
 template <typename A>
-__device__ __forceinline__ int row_slot(const A& a, int n, int lane, int* row, int* position) {
-  const int b = a.seq_idx[n], p = a.pos[n];
+__device__ __forceinline__ int row_slot(const A& a, int b, int p, int* row, bool record) {
   const int lp = a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size;
   const bool ok = b >= 0 && b < a.batch && p >= 0 && lp < a.max_pages;
   const int page = ok ? a.page_table[(size_t)b * a.max_pages + lp] : -1;
   *row = p - lp * a.page_size;
-  *position = p;
   if (page < 0 || page >= a.num_pages) {
-    if (lane == 0) record_status(a.status, MLA_ERR_BOUNDS);
+    if (record) record_status(a.status, MLA_ERR_BOUNDS);
     return -1;
   }
   return page;
@@ -115,10 +113,24 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&x)[16]) 
   }
 }
 
+// of values >= 0, whose bit patterns are ordered as they are
 __device__ __forceinline__ float warp_max(float v) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
+// 16 elements as they lie in memory, for a load ahead of its use
+template <typename T>
+struct Raw16 {
+  uint4 v[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(const T* p, Raw16<T>& r) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  for (int i = 0; i < (int)sizeof(T); ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+}
+template <typename T>
+__device__ __forceinline__ void unpack16(const Raw16<T>& r, float (&x)[16]) {
+  load16<true>(reinterpret_cast<const T*>(r.v), x);
 }
 
 // RMSNorm of one token's c, held 16 elements per lane and block: y = c w r,
@@ -126,8 +138,8 @@ __device__ __forceinline__ float warp_max(float v) {
 // borders bf16 inputs meet exactly, so y is the correctly rounded fp32 value up to
 // an error of 2^-48: the sum and r are formed in 64 bits, c w as a product and
 // its remainder, r as the sum of two floats.
-template <typename T, int NB, bool VEC>
-__device__ __forceinline__ void rms_norm(const RowsArgs& a, int lane, int nb, float (&x)[NB][16]) {
+template <typename T, int NB, bool VEC, bool AHEAD>
+__device__ __forceinline__ void rms_norm(const RowsArgs& a, int lane, int nb, const Raw16<T>& w0, float (&x)[NB][16]) {
   double ss = 0.0;
 #pragma unroll
   for (int j = 0; j < NB; ++j)
@@ -138,14 +150,15 @@ __device__ __forceinline__ void rms_norm(const RowsArgs& a, int lane, int nb, fl
     }
 #pragma unroll
   for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const double r = rsqrt(ss / (double)a.d_c + a.norm_eps);
+  const double r = rsqrt(fma(ss, a.inv_dc, a.norm_eps));
   const float r_hi = (float)r, r_lo = (float)(r - (double)r_hi);
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     const int b = lane + 32 * j;
     if (b < nb) {
       float w[16];
-      load16<VEC>(static_cast<const T*>(a.norm_w) + 16 * b, w);
+      if (AHEAD) unpack16(w0, w);
+      else load16<VEC>(static_cast<const T*>(a.norm_w) + 16 * b, w);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float p = x[j][e] * w[e];
@@ -202,7 +215,7 @@ __device__ __forceinline__ void store_fp4(uint8_t* pg, const Fp4Page& f4, int pr
 // T: type of the rows; CACHE: cache type; NB: blocks per lane (d_c <= 512 NB);
 // VEC: rows, weights and unquantised cache rows allow 16-byte accesses.
 template <typename T, int CACHE, int NB, bool VEC>
-__global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) append_rows_kernel(const __grid_constant__ RowsArgs a) {
   pdl_trigger();
   pdl_wait();
   tl_begin(a.timeline, MLA_TRACE_APPEND_FINALIZE);
@@ -211,77 +224,106 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_cons
   const double inv0 = lane < half ? (half <= kMaxHalf ? a.inv_freq[lane & (kMaxHalf - 1)]
                                                       : rope_inv_freq(lane, half, a.rope_base))
                                   : 0.0;
-  for (int n = blockIdx.x * kWarps + (threadIdx.x >> 5); n < a.n_tokens; n += gridDim.x * kWarps) {
-    int prow, position;
-    const int page = row_slot(a, n, lane, &prow, &position);
-    if (page < 0) continue;
-    const T* src = static_cast<const T*>(a.c) + (long long)n * a.c_stride;
+  // bf16 rows of at most 512 elements: the weights stay in registers, and the
+  // next token's row is loaded while this one is computed
+  constexpr bool kAhead = VEC && NB == 1 && sizeof(T) == 2;
+  const int stride = gridDim.x * kWarps, last = a.n_tokens - 1;
+  int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (n > last) return tl_end(a.timeline, MLA_TRACE_APPEND_FINALIZE);
+  Raw16<T> raw = {}, w0 = {};
+  T k1 = from_f<T>(0.f), k2 = k1;
+  auto fetch = [&](int m) {
+    if (kAhead && lane < nb) load_raw(static_cast<const T*>(a.c) + (long long)m * a.c_stride + 16 * lane, raw);
+    if (lane < half) {
+      const T* p = static_cast<const T*>(a.kr) + (long long)m * a.kr_stride;
+      k1 = p[lane];
+      k2 = p[lane + half];
+    }
+  };
+  if (kAhead && a.norm_w && lane < nb) load_raw(static_cast<const T*>(a.norm_w) + 16 * lane, w0);
+  fetch(n);
+  int position = a.pos[n], prow;
+  int page = row_slot(a, a.seq_idx[n], position, &prow, lane == 0);
+  for (; n <= last; n += stride) {
     float x[NB][16];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int b = lane + 32 * j;
-      if (b < nb) {
-        load16<VEC>(src + 16 * b, x[j]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[j][e] = 0.f;
-      }
-    }
-    uint8_t* pg = a.pool + (size_t)page * a.page_bytes;
-    CT* kr = CACHE == MLA_F32 || CACHE == MLA_BF16
-                 ? reinterpret_cast<CT*>(pg) + (size_t)prow * (a.d_c + a.d_rope) + a.d_c
-                 : reinterpret_cast<CT*>(pg + coded_kr_off(CACHE, a.page_size, a.d_c, a.d_rope)) + (size_t)prow * a.d_rope;
-    const T* krs = static_cast<const T*>(a.kr) + (long long)n * a.kr_stride;
-    float kr_max = 0.f;
-    for (int i = lane; i < half; i += 32) {
-      const double inv = i == lane ? inv0
-                         : half <= kMaxHalf ? a.inv_freq[i & (kMaxHalf - 1)]
-                                            : rope_inv_freq(i, half, a.rope_base);
-      float cs, sn;
-      rope_cos_sin_at(position, inv, &cs, &sn);
-      const float x1 = to_f(krs[i]), x2 = to_f(krs[i + half]);
-      const CT y1 = from_f<CT>(x1 * cs - x2 * sn), y2 = from_f<CT>(x2 * cs + x1 * sn);
-      kr[i] = y1;
-      kr[i + half] = y2;
-      bool f = true;
-      kr_max = fmaxf(kr_max, fmaxf(finite_abs(to_f(y1), f), finite_abs(to_f(y2), f)));
-    }
-    if (a.norm_w) rms_norm<T, NB, VEC>(a, lane, nb, x);
-    if (CACHE == MLA_FP4_E2M1) {
-      store_fp4<NB>(pg, fp4_page(a.page_size, a.d_c, a.d_rope), prow, a.d_c, lane, nb, x, warp_max(kr_max));
-    } else if (CACHE == MLA_FP8_E4M3) {
-      // tiles of 128 columns: eight lanes each, the quantiser of the FP8 append
-      const Fp8Page fp = fp8_page(a.page_size, a.d_c, a.d_rope);
+    if (kAhead) {
+      unpack16(raw, x[0]);
+    } else {
+      const T* src = static_cast<const T*>(a.c) + (long long)n * a.c_stride;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int b = lane + 32 * j;
-        float amax = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[j][e]));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float scale = amax > 0.f ? amax / kE4M3Max : 1.0f;
         if (b < nb) {
-          uint32_t w[4];
+          load16<VEC>(src + 16 * b, x[j]);
+        } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            w[q] = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[q] |= (uint32_t)__nv_cvt_float_to_fp8(x[j][4 * q + e] / scale, __NV_SATFINITE, __NV_E4M3) << (8 * e);
-          }
-          *reinterpret_cast<uint4*>(pg + (size_t)prow * a.d_c + 16 * b) = make_uint4(w[0], w[1], w[2], w[3]);
-          if ((b & 7) == 0) reinterpret_cast<float*>(pg + fp.sc_off)[(size_t)prow * (a.d_c / 128) + b / 8] = scale;
+          for (int e = 0; e < 16; ++e) x[j][e] = 0.f;
         }
       }
-    } else {
-      CT* dst = reinterpret_cast<CT*>(pg) + (size_t)prow * (a.d_c + a.d_rope);
+    }
+    const float x1_0 = to_f(k1), x2_0 = to_f(k2);
+    // the next token's row, position and sequence; its page after this row
+    const int m = min(n + stride, last), m_pos = a.pos[m], m_seq = a.seq_idx[m];
+    fetch(m);
+    if (page >= 0) {
+      uint8_t* pg = a.pool + (size_t)page * a.page_bytes;
+      CT* kr = CACHE == MLA_F32 || CACHE == MLA_BF16
+                   ? reinterpret_cast<CT*>(pg) + (size_t)prow * (a.d_c + a.d_rope) + a.d_c
+                   : reinterpret_cast<CT*>(pg + coded_kr_off(CACHE, a.page_size, a.d_c, a.d_rope)) + (size_t)prow * a.d_rope;
+      const T* krs = static_cast<const T*>(a.kr) + (long long)n * a.kr_stride;
+      float kr_max = 0.f;
+      for (int i = lane; i < half; i += 32) {
+        const double inv = i == lane ? inv0
+                           : half <= kMaxHalf ? a.inv_freq[i & (kMaxHalf - 1)]
+                                              : rope_inv_freq(i, half, a.rope_base);
+        float cs, sn;
+        rope_cos_sin_at(position, inv, &cs, &sn);
+        const float x1 = i == lane ? x1_0 : to_f(krs[i]), x2 = i == lane ? x2_0 : to_f(krs[i + half]);
+        const CT y1 = from_f<CT>(x1 * cs - x2 * sn), y2 = from_f<CT>(x2 * cs + x1 * sn);
+        kr[i] = y1;
+        kr[i + half] = y2;
+        bool f = true;
+        kr_max = fmaxf(kr_max, fmaxf(finite_abs(to_f(y1), f), finite_abs(to_f(y2), f)));
+      }
+      if (a.norm_w) rms_norm<T, NB, VEC, kAhead>(a, lane, nb, w0, x);
+      if (CACHE == MLA_FP4_E2M1) {
+        store_fp4<NB>(pg, fp4_page(a.page_size, a.d_c, a.d_rope), prow, a.d_c, lane, nb, x, warp_max(kr_max));
+      } else if (CACHE == MLA_FP8_E4M3) {
+        // tiles of 128 columns: eight lanes each, the quantiser of the FP8 append
+        const Fp8Page fp = fp8_page(a.page_size, a.d_c, a.d_rope);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int b = lane + 32 * j;
-        if (b < nb) store16<VEC>(dst + 16 * b, x[j]);
+        for (int j = 0; j < NB; ++j) {
+          const int b = lane + 32 * j;
+          float amax = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[j][e]));
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const float scale = amax > 0.f ? amax / kE4M3Max : 1.0f;
+          if (b < nb) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              w[q] = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[q] |= (uint32_t)__nv_cvt_float_to_fp8(x[j][4 * q + e] / scale, __NV_SATFINITE, __NV_E4M3) << (8 * e);
+            }
+            *reinterpret_cast<uint4*>(pg + (size_t)prow * a.d_c + 16 * b) = make_uint4(w[0], w[1], w[2], w[3]);
+            if ((b & 7) == 0) reinterpret_cast<float*>(pg + fp.sc_off)[(size_t)prow * (a.d_c / 128) + b / 8] = scale;
+          }
+        }
+      } else {
+        CT* dst = reinterpret_cast<CT*>(pg) + (size_t)prow * (a.d_c + a.d_rope);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const int b = lane + 32 * j;
+          if (b < nb) store16<VEC>(dst + 16 * b, x[j]);
+        }
       }
     }
+    position = m_pos;
+    page = n + stride <= last ? row_slot(a, m_seq, m_pos, &prow, lane == 0) : -1;
   }
   tl_end(a.timeline, MLA_TRACE_APPEND_FINALIZE);
 }
@@ -295,8 +337,8 @@ __global__ void __launch_bounds__(kThreads) append_fp4_finalize_kernel(const __g
   tl_begin(a.timeline, MLA_TRACE_APPEND_FINALIZE);
   const int lane = threadIdx.x & 31, nb = a.d_c / 16;
   const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  int prow, position;
-  const int page = n < a.n_tokens ? row_slot(a, n, lane, &prow, &position) : -1;
+  int prow;
+  const int page = n < a.n_tokens ? row_slot(a, a.seq_idx[n], a.pos[n], &prow, lane == 0) : -1;
   if (page >= 0) {
     const Fp4Page f4 = fp4_page(a.page_size, a.d_c, a.d_rope);
     uint8_t* pg = a.pool + (size_t)page * a.page_bytes;
@@ -334,66 +376,165 @@ struct ReadArgs {
   int* status;
 };
 
-template <typename TO, int CACHE, bool VEC>
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __float22bfloat162_rn(v);
+}
+
+// Eight elements of a cache row: their bytes, then their values.  A lane takes
+// eight, not a block of 16, so that a warp's 16-byte stores fill whole sectors.
+template <int CACHE, bool VEC>
+struct CacheUnit {
+  using CT = typename std::conditional<CACHE == MLA_F32, float, __nv_bfloat16>::type;
+  float x[8];
+  __device__ __forceinline__ void load(const ReadArgs& a, const uint8_t* pg, int prow, int b) {
+    const CT* p = reinterpret_cast<const CT*>(pg) + (size_t)prow * (a.d_c + a.d_rope) + 8 * b;
+    if (VEC) {
+      load8(p, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = to_f(p[e]);
+    }
+  }
+  __device__ __forceinline__ void values(float (&y)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[e];
+  }
+};
+template <bool VEC>
+struct CacheUnit<MLA_FP8_E4M3, VEC> {
+  uint2 w;
+  float s;
+  __device__ __forceinline__ void load(const ReadArgs& a, const uint8_t* pg, int prow, int b) {
+    w = *reinterpret_cast<const uint2*>(pg + (size_t)prow * a.d_c + 8 * b);
+    s = reinterpret_cast<const float*>(pg + fp8_page(a.page_size, a.d_c, a.d_rope).sc_off)[prow * (a.d_c / 128) + b / 16];
+  }
+  __device__ __forceinline__ void values(float (&y)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = e4m3_to_float((uint8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3)))) * s;
+  }
+};
+template <bool VEC>
+struct CacheUnit<MLA_FP4_E2M1, VEC> {
+  uint32_t w;
+  float ts;
+  uint8_t sc;
+  __device__ __forceinline__ void load(const ReadArgs& a, const uint8_t* pg, int prow, int b) {
+    const Fp4Page f4 = fp4_page(a.page_size, a.d_c, a.d_rope);
+    w = *reinterpret_cast<const uint32_t*>(pg + prow * (a.d_c / 2) + 4 * b);
+    sc = pg[f4.sc_off + prow * (a.d_c / 16) + b / 2];
+    ts = reinterpret_cast<const float*>(pg + f4.ts_off)[prow];
+  }
+  __device__ __forceinline__ void values(float (&y)[8]) const {
+    const float s = e4m3_to_float(sc) * ts;
+    uint32_t h[4];
+    e2m1x8_to_f16x2(w, h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = f16x2_to_float2(h[e]);
+      y[2 * e] = f.x * s;
+      y[2 * e + 1] = f.y * s;
+    }
+  }
+};
+template <bool VEC>
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  if (VEC) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = x[e];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  if (VEC) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+      w[e] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = __float2bfloat16_rn(x[e]);
+  }
+}
+
+// A warp takes U consecutive tokens of the list: their slots are resolved side
+// by side, one lane each, and all their loads are issued before the first is used.
+template <typename TO, int CACHE, bool VEC, int U>
 __global__ void __launch_bounds__(kThreads) read_rows_kernel(const __grid_constant__ ReadArgs a) {
   pdl_trigger();
   pdl_wait();
   using CT = typename std::conditional<CACHE == MLA_F32, float, __nv_bfloat16>::type;
-  const int lane = threadIdx.x & 31, nb = a.d_c / 16;
-  for (int n = blockIdx.x * kWarps + (threadIdx.x >> 5); n < a.n_tokens; n += gridDim.x * kWarps) {
-    int prow, position;
-    const int page = row_slot(a, n, lane, &prow, &position);
-    if (page < 0) continue;
-    const uint8_t* pg = a.pool + (size_t)page * a.page_bytes;
-    const CT* kr;
-    if (CACHE == MLA_F32 || CACHE == MLA_BF16) {
-      const CT* row = reinterpret_cast<const CT*>(pg) + (size_t)prow * (a.d_c + a.d_rope);
-      kr = row + a.d_c;
-      for (int b = lane; b < nb; b += 32) {
-        float x[16];
-        load16<VEC>(row + 16 * b, x);
-        store16<VEC>(static_cast<TO*>(a.c_out) + (size_t)n * a.d_c + 16 * b, x);
-      }
-    } else {
-      kr = reinterpret_cast<const CT*>(pg + coded_kr_off(CACHE, a.page_size, a.d_c, a.d_rope)) + (size_t)prow * a.d_rope;
-      for (int b = lane; b < nb; b += 32) {
-        float x[16];
-        if (CACHE == MLA_FP4_E2M1) {
-          const Fp4Page f4 = fp4_page(a.page_size, a.d_c, a.d_rope);
-          const uint2 w = *reinterpret_cast<const uint2*>(pg + (size_t)prow * (a.d_c / 2) + 8 * b);
-          const float s = e4m3_to_float(pg[f4.sc_off + (size_t)prow * (a.d_c / 16) + b]) *
-                          reinterpret_cast<const float*>(pg + f4.ts_off)[prow];
-          uint32_t h[8];
-          e2m1x8_to_f16x2(w.x, *reinterpret_cast<uint32_t(*)[4]>(&h[0]));
-          e2m1x8_to_f16x2(w.y, *reinterpret_cast<uint32_t(*)[4]>(&h[4]));
+  const int lane = threadIdx.x & 31, nu = a.d_c / 8;
+  constexpr bool kCoded = CACHE == MLA_FP8_E4M3 || CACHE == MLA_FP4_E2M1;
+  const size_t kr_off = kCoded ? coded_kr_off(CACHE, a.page_size, a.d_c, a.d_rope) : (size_t)a.d_c * sizeof(CT);
+  const int kr_row = kCoded ? a.d_rope : a.d_c + a.d_rope;
+  for (long long n0 = (long long)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * U; n0 < a.n_tokens;
+       n0 += (long long)gridDim.x * kWarps * U) {
+    int my_page = -1, my_row = 0;
+    if (lane < U && n0 + lane < a.n_tokens) my_page = row_slot(a, a.seq_idx[n0 + lane], a.pos[n0 + lane], &my_row, true);
+    const uint8_t* pg[U];
+    int prow[U];
+    bool ok[U];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 f = f16x2_to_float2(h[e]);
-            x[2 * e] = f.x * s;
-            x[2 * e + 1] = f.y * s;
-          }
-        } else {
-          const Fp8Page fp = fp8_page(a.page_size, a.d_c, a.d_rope);
-          const uint4 w = *reinterpret_cast<const uint4*>(pg + (size_t)prow * a.d_c + 16 * b);
-          const float s = reinterpret_cast<const float*>(pg + fp.sc_off)[(size_t)prow * (a.d_c / 128) + b / 8];
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = e4m3_to_float((uint8_t)(ww[e >> 2] >> (8 * (e & 3)))) * s;
-        }
-        store16<VEC>(static_cast<TO*>(a.c_out) + (size_t)n * a.d_c + 16 * b, x);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int page = __shfl_sync(0xffffffffu, my_page, u);
+      prow[u] = __shfl_sync(0xffffffffu, my_row, u);
+      ok[u] = page >= 0;
+      pg[u] = a.pool + (size_t)(ok[u] ? page : 0) * a.page_bytes;
     }
-    TO* ko = static_cast<TO*>(a.kr_out) + (size_t)n * a.d_rope;
-    for (int i = lane; i < a.d_rope; i += 32) ko[i] = from_f<TO>(to_f(kr[i]));
+    for (int i = VEC ? 2 * lane : lane; i < a.d_rope; i += VEC ? 64 : 32) {
+      float2 k[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (ok[u]) {
+          const CT* p = reinterpret_cast<const CT*>(pg[u] + kr_off) + (size_t)prow[u] * kr_row + i;
+          if (VEC) k[u] = load2(p);
+          else k[u].x = to_f(*p);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (ok[u]) {
+          TO* p = static_cast<TO*>(a.kr_out) + (size_t)(n0 + u) * a.d_rope + i;
+          if (VEC) store2(p, k[u]);
+          else *p = from_f<TO>(k[u].x);
+        }
+    }
+    for (int b = lane; b < nu; b += 64) {
+      CacheUnit<CACHE, VEC> unit[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (ok[u] && b + 32 * j < nu) unit[u][j].load(a, pg[u], prow[u], b + 32 * j);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (ok[u] && b + 32 * j < nu) {
+            float y[8];
+            unit[u][j].values(y);
+            store8<VEC>(static_cast<TO*>(a.c_out) + (size_t)(n0 + u) * a.d_c + 8 * (b + 32 * j), y);
+          }
+    }
   }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// One warp per token, up to 32 CTAs per SM, then every warp loops.
-int rows_grid(int n_tokens) {
-  const int ctas = (n_tokens + kWarps - 1) / kWarps, most = 32 * device_sm_count();
-  return ctas < most ? ctas : most;
+// One warp per per_warp tokens, up to `most` CTAs per SM, then every warp loops.
+int rows_grid(int n_tokens, int per_warp, int most) {
+  const int ctas = (n_tokens - 1) / (kWarps * per_warp) + 1;
+  return ctas < most * device_sm_count() ? ctas : most * device_sm_count();
 }
 
 // log2 of a page size that is a power of two, else -1.
@@ -407,13 +548,18 @@ template <typename T, int CACHE>
 cudaError_t launch_rows_typed(const RowsArgs& a, bool vec, cudaStream_t st) {
   auto kernel = a.d_c <= 512 ? (vec ? append_rows_kernel<T, CACHE, 1, true> : append_rows_kernel<T, CACHE, 1, false>)
                              : (vec ? append_rows_kernel<T, CACHE, 2, true> : append_rows_kernel<T, CACHE, 2, false>);
-  return launch_pdl(kernel, dim3(rows_grid(a.n_tokens)), dim3(kThreads), 0, st, a);
+  return launch_pdl(kernel, dim3(rows_grid(a.n_tokens, 1, 3)), dim3(kThreads), 0, st, a);
 }
 
 template <typename TO, int CACHE>
 cudaError_t launch_read_typed(const ReadArgs& a, bool vec, cudaStream_t st) {
-  auto kernel = vec ? read_rows_kernel<TO, CACHE, true> : read_rows_kernel<TO, CACHE, false>;
-  return launch_pdl(kernel, dim3(rows_grid(a.n_tokens)), dim3(kThreads), 0, st, a);
+  // four tokens a warp once that still gives every SM four CTAs
+  if (a.n_tokens >= 4 * 4 * kWarps * device_sm_count()) {
+    auto kernel = vec ? read_rows_kernel<TO, CACHE, true, 4> : read_rows_kernel<TO, CACHE, false, 4>;
+    return launch_pdl(kernel, dim3(rows_grid(a.n_tokens, 4, 32)), dim3(kThreads), 0, st, a);
+  }
+  auto kernel = vec ? read_rows_kernel<TO, CACHE, true, 1> : read_rows_kernel<TO, CACHE, false, 1>;
+  return launch_pdl(kernel, dim3(rows_grid(a.n_tokens, 1, 32)), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace
@@ -466,6 +612,7 @@ extern "C" int mla_append_rows(const mla_dims* dims, const void* c, int64_t c_st
   a.kr_stride = k_stride;
   a.norm_w = norm_weight;
   a.norm_eps = (double)norm_eps;
+  a.inv_dc = 1.0 / (double)dims->d_c;
   a.n_tokens = n_tokens;
   a.seq_idx = seq_idx;
   a.pos = pos;
@@ -543,7 +690,7 @@ extern "C" int mla_read_rows(const mla_dims* dims, const void* cache_pool, int n
   a.status = device_status_word();
   // output rows of c are d_c (a multiple of 16) elements apart
   const size_t cs = dims->cache_dtype == MLA_F32 ? 4 : 2;
-  bool vec = aligned16(c_out);
+  bool vec = aligned16(c_out) && aligned16(k_out) && dims->d_rope % 2 == 0;
   if (!is_coded_cache(*dims))
     vec = vec && (size_t)(dims->d_c + dims->d_rope) * cs % 16 == 0 && a.page_bytes % 16 == 0;
   cudaStream_t st = (cudaStream_t)stream;
