@@ -91,7 +91,8 @@ enum {
  *     MMA issuers' and softmax warps' bounded waits (~2 s) expire; the CTA
  *     pair that gives up first tells its peer, every role stops, the kernel
  *     waits (bounded) for the MMAs it issued and frees its tensor memory;
- *     MLA_ERR_TIMEOUT is recorded and the split partials are not valid.
+ *     MLA_ERR_TIMEOUT is recorded and the split partials are not valid.  The
+ *     few-row kernel over a 4-bit cache does the same within its CTA.
  *   - mla_combine: the kernel does not fetch its weights, so its bounded wait
  *     for them expires; MLA_ERR_TIMEOUT is recorded and out and lse_out are
  *     left unwritten.
@@ -256,6 +257,12 @@ int mla_read_rows(const mla_dims* dims, const void* cache_pool, int num_pages,
  *   seq_lens   [batch] int32, tokens in the cache per sequence (>= n_q)
  *   num_splits number of key-range splits shared by all sequences; 0 = auto
  *   workspace  >= mla_decode_workspace_bytes(dims, batch, n_q, num_splits)
+ * Head counts: the CUDA-core kernel takes multiples of 4, the tensor-core kernels
+ * over a 4-bit cache any (mla_decode_path).
+ * Range: the tensor-core kernels over an FP8 or 4-bit cache hold q~ and the
+ * probabilities as f16, and all but the few-row kernel (path 2) the latent too:
+ * |q~| and |c| up to 65504, and where a token's largest |c| is below 2^-15 its
+ * small elements lose bits (absolute error up to 2^-25).
  * The workspace is consumed by the next mla_combine with the same dims, batch,
  * n_q and num_splits.
  * ------------------------------------------------------------------------- */
@@ -272,7 +279,8 @@ int mla_decode(const mla_dims* dims, const void* q_nope, const void* q_rope,
  *   o_h = W_uv[h] u_h  ("value aggregation ... directly against c", with W^UV
  *                       applied after the softmax, as in the decoding module)
  *   W_uv    [n_heads, d_v, d_c] act
- *   out     [batch, n_q, n_heads, d_v] act, written
+ *   out     [batch, n_q, n_heads, d_v] act, written; 4-byte aligned where
+ *           mla_decode_path is 1 or 2 (MLA_ERR_ALIGNMENT otherwise)
  *   lse_out [batch, n_q, n_heads] float32 natural-log softmax denominators of
  *           the scaled scores, written; may be NULL
  * `workspace`, `batch`, `n_q`, `num_splits` as passed to the mla_decode call
@@ -319,7 +327,11 @@ int mla_prefill(const mla_dims* dims, const void* q_nope, const void* q_rope,
                 void* out, float* lse_out, void* stream);
 
 /* Which decode kernel mla_decode would launch for these dims on the current
- * device: 0 = CUDA-core (SIMT) kernel, 1 = tcgen05 kernel; <0 = error code. */
+ * device: 0 = CUDA-core (SIMT) kernel, 1 = tcgen05 kernel (bf16 activations at
+ * DeepSeek-V3's d_c 512, d_rope 64, d_v 128 and 64-token pages: 128 heads and up
+ * to 8 query tokens over a bf16 or FP8 cache, more than 16 rows (heads times
+ * query tokens) over a 4-bit cache), 2 = warp-level MMA kernel (a 4-bit cache, the
+ * same dims, at most 16 rows); <0 = error code. */
 int mla_decode_path(const mla_dims* dims, int n_q);
 
 /* Number of key-range splits that num_splits = 0 selects on the current device. */

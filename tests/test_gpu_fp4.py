@@ -262,3 +262,45 @@ def test_more_heads_than_multiprocessors(heads, cache):
     for b in range(cfg.B):
         o, _ = op.expected_absorbed(b, cache=caches[b])
         assert rel_err(out[b].double().cpu().numpy(), o) <= 1e-2
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("d_v", [64, 136])
+def test_other_value_widths_at_128_heads(cache, d_v):
+    """The tensor-core decode's partials are bf16 rows that only the combine of d_v = 128 reads."""
+    cfg = fp4_cfg(cache_dtype=cache, B=2, T=1, L=(70, 200), d_v=d_v)
+    gp = GpuProblem(cfg)
+    assert B.decode_path(gp.dims, 1) == 0
+    gp.session.append(gp.inputs["h"], gp.seq_idx, gp.pos, gp.weights["W_dkv"], gp.weights["W_kr"], gp.page_table,
+                      gp.cache.pool)
+    out, lse = gp.attend_only()
+    assert gp.status() == 0
+    op = Fp4Oracle(cfg)
+    c, kr = gp.cache.values(*every_position(cfg), gp.page_table)
+    at = 0
+    for b in range(cfg.B):
+        n = int(cfg.seq_lens[b])
+        o, l, _ = O.decode_absorbed(op.inp["q_nope"][b], op.inp["q_rope"][b], c[at:at + n].double().cpu().numpy(),
+                                    kr[at:at + n].double().cpu().numpy(), op.w["W_uk"], op.w["W_uv"], n,
+                                    cfg.softmax_scale, cfg.rope_base)
+        at += n
+        assert rel_err(out[b].double().cpu().numpy(), o) <= tolerance(cfg), b
+
+
+def every_position(cfg):
+    seq = np.concatenate([np.full(int(n), b, np.int32) for b, n in enumerate(cfg.seq_lens)])
+    pos = np.concatenate([np.arange(int(n), dtype=np.int32) for n in cfg.seq_lens])
+    return torch.from_numpy(seq).cuda(), torch.from_numpy(pos).cuda()
+
+
+@pytest.mark.parametrize("cache,heads", [("bf16", 128), ("fp8", 128), ("fp4", 128), ("fp4", 8)])
+def test_combine_refuses_an_output_that_holds_no_pairs(cache, heads):
+    cfg = fp4_cfg(cache_dtype=cache, B=1, T=1, L=(70,), n_heads=heads)
+    gp = GpuProblem(cfg)
+    assert B.decode_path(gp.dims, 1) >= 1
+    out, _ = gp.attend_only()
+    odd = torch.zeros(out.numel() + 1, dtype=out.dtype, device="cuda")[1:]
+    ws = torch.zeros(B.decode_workspace_bytes(gp.dims, 1, 1, 0), dtype=torch.uint8, device="cuda")
+    with pytest.raises(B.MlaError, match="ALIGN"):
+        B.mla_combine(gp.dims, gp.weights["W_uv"], 1, 1, ws, odd.view(out.shape))
+    assert odd.abs().sum().item() == 0 and gp.status() == 0
