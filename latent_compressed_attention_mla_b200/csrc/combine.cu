@@ -148,15 +148,16 @@ struct CombineTcArgs {
   float* lse_out;
   int* status;
   int n_heads, batch, n_q;
+  int block;          // tokens of a block, at most TOK
   int stall;          // self-test: the weight fetch is not issued (its wait expires)
   unsigned long long* timeline;  // device timeline (null: off)
   CUtensorMap map_w;  // W_uv as [n_heads * d_v rows][d_c] bf16, box 64 x 128, 128-byte swizzle
 };
 
-// W^UV_h, the bf16 u tile and, for 16-token blocks, the fp32 scratch of the
-// groups' sums
-size_t combine_tc_smem(int tok) {
-  return kTcWBytes + (size_t)tok * kTcDc * 2 + (tok == 16 ? (size_t)tok * kTcDc * 4 : 0) + 1024;
+// W^UV_h, the bf16 u tile (two of them for u in two terms) and, for 16-token
+// blocks, the fp32 scratch of the groups' sums
+size_t combine_tc_smem(int tok, bool two_terms) {
+  return kTcWBytes + (size_t)tok * kTcDc * (two_terms ? 4 : 2) + (tok == 16 ? (size_t)tok * kTcDc * 4 : 0) + 1024;
 }
 
 // W^UV_h (d_v rows x d_c columns) arrives by eight TMA boxes into [8 column
@@ -166,8 +167,8 @@ size_t combine_tc_smem(int tok) {
 // A 16-byte piece of a split partial row: eight bf16 or four fp32 columns.
 // Loads bring raw pieces into registers; the conversion to fp32 happens only
 // when they are used, so that all of a round's loads are in flight together.
-template <bool PB> struct PartUnit;
-template <> struct PartUnit<true> {
+template <PartType PT> struct PartUnit;
+template <> struct PartUnit<kPartBf16> {
   static constexpr int kCols = 8;
   __device__ static uint4 load(const float* o_part, size_t row, int c0) {
     return *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(o_part) + row * 512 + c0);
@@ -182,7 +183,22 @@ template <> struct PartUnit<true> {
     }
   }
 };
-template <> struct PartUnit<false> {
+template <> struct PartUnit<kPartF16> {
+  static constexpr int kCols = 8;
+  __device__ static uint4 load(const float* o_part, size_t row, int c0) {
+    return *reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(o_part) + row * 512 + c0);
+  }
+  __device__ static void to_float(const uint4& x, float (&v)[8]) {
+    const __half2* h = reinterpret_cast<const __half2*>(&x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
+template <> struct PartUnit<kPartF32> {
   static constexpr int kCols = 4;
   __device__ static uint4 load(const float* o_part, size_t row, int c0) {
     return *reinterpret_cast<const uint4*>(o_part + row * 512 + c0);
@@ -195,11 +211,29 @@ template <> struct PartUnit<false> {
   }
 };
 
-// PB: the split partials are bf16 (written by the tensor-core decode), else fp32.
-template <int TOK, bool PB>
+// Four values of u as bf16, and (TWO) their remainders as bf16 `bytes` further on.
+template <bool TWO>
+__device__ __forceinline__ void store_u4(uint8_t* dst, int bytes, float a, float b, float c, float d) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  if (TWO) {
+    const float2 l = __bfloat1622float2(lo), h = __bfloat1622float2(hi);
+    const __nv_bfloat162 rl = __floats2bfloat162_rn(a - l.x, b - l.y), rh = __floats2bfloat162_rn(c - h.x, d - h.y);
+    *reinterpret_cast<uint2*>(dst + bytes) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&rl), *reinterpret_cast<const uint32_t*>(&rh));
+  }
+}
+
+// PT: type of the split partials.  TWO: u enters the product as a bf16 value and the
+// bf16 of its remainder (two MMAs; u's own rounding then is 2^-17, not 2^-9).  With
+// f16 or fp32 partials the step's error against 64 bits is that of the output's own
+// rounding, 1.7e-3 rms, not 2.6e-3; at 128 heads and 256 query rows the kernel
+// takes 81 us for 60 (of a 1.44 ms step; blocks of 32 tokens, since the second tile
+// takes the room of blocks of 64).
+template <int TOK, PartType PT, bool TWO>
 __global__ void __launch_bounds__(kThreads) combine_tc_kernel(const __grid_constant__ CombineTcArgs P) {
   static_assert(TOK % 16 == 0 && TOK <= 64, "token block");
-  using PU = PartUnit<PB>;
+  using PU = PartUnit<PT>;
   constexpr int kCU = PU::kCols;            // columns per 16-byte load
   constexpr int kUnits = kTcDc / kCU;       // loads per partial row
   constexpr int kGroups = kThreads / kUnits;  // threads per column unit (token groups / split groups)
@@ -218,6 +252,7 @@ __global__ void __launch_bounds__(kThreads) combine_tc_kernel(const __grid_const
   const int32_t* plan = P.plan;
   uint8_t* Ws = smem;              // [8][d_v][128 B]
   uint8_t* Us = smem + kTcWBytes;  // [8][TOK][128 B]
+  constexpr int kUBytes = TOK * kTcDc * 2;  // TWO: the remainders' tile follows
   const int M = batch * n_q;
   const uint32_t bar = smem_addr(&wbar);
   if (tid == 0) mbar_init_local(bar, 1);
@@ -234,10 +269,10 @@ __global__ void __launch_bounds__(kThreads) combine_tc_kernel(const __grid_const
   tl_begin(P.timeline, MLA_TRACE_COMBINE);
   const int splits = plan[batch + 2];
   const int n_slots = batch + splits - 1;  // slot stride of the decode that wrote the partials
-  // token blocks blockIdx.y, blockIdx.y + gridDim.y, ... of TOK tokens; W^UV_h
-  // stays in shared memory for all of them
-  for (int m0 = blockIdx.y * TOK; m0 < M; m0 += gridDim.y * TOK) {
-    const int mc = min(TOK, M - m0);
+  // token blocks blockIdx.y, blockIdx.y + gridDim.y, ...; W^UV_h stays in shared
+  // memory for all of them
+  for (int m0 = blockIdx.y * P.block; m0 < M; m0 += gridDim.y * P.block) {
+    const int mc = min(P.block, M - m0);
     // first slot row (t * n_slots + first split + b) and split count per token;
     // tokens past the end take no split
     if (tid < TOK) {
@@ -297,12 +332,8 @@ __global__ void __launch_bounds__(kThreads) combine_tc_kernel(const __grid_const
       // kCU columns of token mi as bf16 into the swizzled u tile
 #pragma unroll
       for (int e = 0; e < kCU; e += 4) {
-        const __nv_bfloat162 lo2 = __floats2bfloat162_rn(a[e], a[e + 1]);
-        const __nv_bfloat162 hi2 = __floats2bfloat162_rn(a[e + 2], a[e + 3]);
-        uint2 pk;
-        pk.x = *reinterpret_cast<const uint32_t*>(&lo2);
-        pk.y = *reinterpret_cast<const uint32_t*>(&hi2);
-        *reinterpret_cast<uint2*>(Us + swz_cb(mi, (c0 + e) >> 3, TOK) + ((c0 + e) & 7) * 2) = pk;
+        store_u4<TWO>(Us + swz_cb(mi, (c0 + e) >> 3, TOK) + ((c0 + e) & 7) * 2, kUBytes, a[e], a[e + 1], a[e + 2],
+                      a[e + 3]);
       }
     };
     if constexpr (TOK == 16) {
@@ -310,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) combine_tc_kernel(const __grid_const
       // gr + kGroups, ... of two tokens at a time, eight loads per token in
       // flight (sixteen for a token without a partner); the groups' sums meet
       // in the fp32 scratch R and are added in group order (deterministic)
-      float* R = reinterpret_cast<float*>(Us + TOK * kTcDc * 2);  // [kGroups][2][d_c]
+      float* R = reinterpret_cast<float*>(Us + (TWO ? 2 : 1) * kUBytes);  // [kGroups][2][d_c]
 #pragma unroll 1
       for (int mi0 = 0; mi0 < mc; mi0 += 2) {
         const bool single = s_n[mi0 + 1] == 0;  // the same for the whole CTA
@@ -374,12 +405,7 @@ __global__ void __launch_bounds__(kThreads) combine_tc_kernel(const __grid_const
             sum.z += x.z;
             sum.w += x.w;
           }
-          const __nv_bfloat162 lo2 = __floats2bfloat162_rn(sum.x, sum.y);
-          const __nv_bfloat162 hi2 = __floats2bfloat162_rn(sum.z, sum.w);
-          uint2 pk;
-          pk.x = *reinterpret_cast<const uint32_t*>(&lo2);
-          pk.y = *reinterpret_cast<const uint32_t*>(&hi2);
-          *reinterpret_cast<uint2*>(Us + swz_cb(mi0 + j, c >> 3, TOK) + (c & 7) * 2) = pk;
+          store_u4<TWO>(Us + swz_cb(mi0 + j, c >> 3, TOK) + (c & 7) * 2, kUBytes, sum.x, sum.y, sum.z, sum.w);
         }
         __syncthreads();  // R is rewritten by the next pair
       }
@@ -387,6 +413,7 @@ __global__ void __launch_bounds__(kThreads) combine_tc_kernel(const __grid_const
       for (int i = tid; i < (TOK - ((mc + 1) & ~1)) * (kTcDc / 8); i += kThreads) {
         const int mi = ((mc + 1) & ~1) + i / (kTcDc / 8), u = i % (kTcDc / 8);
         *reinterpret_cast<uint4*>(Us + swz_cb(mi, u, TOK)) = make_uint4(0, 0, 0, 0);
+        if (TWO) *reinterpret_cast<uint4*>(Us + kUBytes + swz_cb(mi, u, TOK)) = make_uint4(0, 0, 0, 0);
       }
     } else {
       // u[m, c0..c0+kCU) = sum_k w_k o_k[c0..c0+kCU) for tokens gr, gr + kGroups, ...
@@ -457,6 +484,11 @@ __global__ void __launch_bounds__(kThreads) combine_tc_kernel(const __grid_const
         load_a_cb(Us, TOK, 16 * i, k0, lane, af);
         mma_bf16(acc[i][0], af, b00, b01);
         mma_bf16(acc[i][1], af, b10, b11);
+        if (TWO) {
+          load_a_cb(Us + kUBytes, TOK, 16 * i, k0, lane, af);
+          mma_bf16(acc[i][0], af, b00, b01);
+          mma_bf16(acc[i][1], af, b10, b11);
+        }
       }
     }
     MLA_STAMP(2);
@@ -487,7 +519,7 @@ int combine_max_splits() { return kMaxSplits; }
 int combine_max_d_c(int act_dtype) { return kMaxVecPerLane * 32 * (act_dtype == MLA_F32 ? 4 : 8); }
 
 cudaError_t launch_combine(const mla_dims& d, const void* W_uv, int batch, int n_q, const int32_t* plan,
-                           const float* o_part, bool part_bf16, const float* lse_part, void* out, float* lse_out,
+                           const float* o_part, PartType part, bool two_terms, const float* lse_part, void* out, float* lse_out,
                            int* status, cudaStream_t st) {
   const size_t smem = combine_smem_bytes(d);
   cudaError_t e;
@@ -516,23 +548,27 @@ cudaError_t launch_combine(const mla_dims& d, const void* W_uv, int batch, int n
     // one CTA per head (W^UV_h fetched once, before the grid-dependency wait,
     // by every CTA at once) looping over blocks of 16, 32 or 64 tokens
     const int M = batch * n_q, sms = device_sm_count();
-    int tok = M > 32 ? 64 : M > 16 ? 32 : 16, blocks_y = 1;
-    if (part_bf16 && 2 * d.n_heads <= sms) {
-      // a shard's few heads: blocks of 32 tokens and several CTAs a head, up to
-      // one a multiprocessor (16 heads, 128 tokens: 35.3 -> 10.9 us; 64 heads,
-      // 64 tokens: 21.4 -> 13.7 us).  Each of a head's CTAs fetches W^UV_h,
-      // 128 KB, again, so blocks of 16 tokens lose: 22.7 and 44.0 us.
-      while (tok > 32 && d.n_heads * ((M + tok - 1) / tok) < sms) tok /= 2;
-      const int blocks = (M + tok - 1) / tok, per_head = sms / d.n_heads;
+    // (two-term u: 32 at most, for whose tiles there is shared memory)
+    int tok = M > 32 && !two_terms ? 64 : M > 16 ? 32 : 16, blocks_y = 1;
+    p.block = tok;
+    if (two_terms && 2 * d.n_heads <= sms) {
+      // a shard's few heads: several CTAs a head, up to one a multiprocessor, and
+      // as many tokens a block as that leaves (16 heads: 128 tokens
+      // 14.7 -> 12.2 us, 8 tokens of 19 splits each 22.6 -> 7.8 us)
+      const int per_head = sms / d.n_heads, share = (M + per_head - 1) / per_head;
+      if (share < tok) p.block = share;
+      const int blocks = (M + p.block - 1) / p.block;
       blocks_y = blocks < per_head ? blocks : per_head;
     }
-    auto kernel = part_bf16 ? (tok == 64   ? combine_tc_kernel<64, true>
-                               : tok == 32 ? combine_tc_kernel<32, true>
-                                           : combine_tc_kernel<16, true>)
-                            : (tok == 64   ? combine_tc_kernel<64, false>
-                               : tok == 32 ? combine_tc_kernel<32, false>
-                                           : combine_tc_kernel<16, false>);
-    const size_t tsm = combine_tc_smem(tok);
+    auto kernel = part == kPartF16 ? (tok == 32 ? combine_tc_kernel<32, kPartF16, true> : combine_tc_kernel<16, kPartF16, true>)
+                  : two_terms      ? (tok == 32 ? combine_tc_kernel<32, kPartF32, true> : combine_tc_kernel<16, kPartF32, true>)
+                  : part == kPartBf16 ? (tok == 64   ? combine_tc_kernel<64, kPartBf16, false>
+                                         : tok == 32 ? combine_tc_kernel<32, kPartBf16, false>
+                                                     : combine_tc_kernel<16, kPartBf16, false>)
+                                      : (tok == 64   ? combine_tc_kernel<64, kPartF32, false>
+                                         : tok == 32 ? combine_tc_kernel<32, kPartF32, false>
+                                                     : combine_tc_kernel<16, kPartF32, false>);
+    const size_t tsm = combine_tc_smem(tok, two_terms);
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tsm);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(d.n_heads, blocks_y), dim3(kThreads), tsm, st, p);

@@ -535,18 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
           if (row >= P.rows) continue;
           const size_t part = ((size_t)t * p.n_slots + (w + s.b)) * p.d.n_heads + (row - t * p.d.n_heads);
           const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
-          uint32_t u[8];
+          // (few rows: fp32 partials cost nothing that shows)
+          float4* dst = reinterpret_cast<float4*>(p.o_part + part * kDC + 64 * ds + 16 * q);
 #pragma unroll
           for (int c = 0; c < 2; ++c)  // columns 16 q + 8 c + j
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[j][2 * r + c] * inv, o[j + 1][2 * r + c] * inv);
-              u[4 * c + j / 2] = *reinterpret_cast<const uint32_t*>(&v2);
-            }
-          // the split partials are bf16 rows on this path (the combine reads them so)
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o_part) + part * kDC + 64 * ds + 16 * q);
-          dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
-          dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
+            for (int j = 0; j < 8; j += 4)
+              dst[2 * c + j / 4] = make_float4(o[j][2 * r + c] * inv, o[j + 1][2 * r + c] * inv, o[j + 2][2 * r + c] * inv,
+                                               o[j + 3][2 * r + c] * inv);
           if (ds == 0 && q == 0) p.lse_part[part] = l[r] > 0.f ? m_ref[r] + __log2f(l[r]) : -INFINITY;
         }
       }

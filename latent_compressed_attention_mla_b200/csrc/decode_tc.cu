@@ -746,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
     uint32_t g = 0;
     bool ok = true;
     while (walk.next(s)) {
-      // the row's place among the split partials, bf16 rows on this path (the combine reads them so)
+      // the row's place among the split partials, 16-bit rows on this path (the combine reads them so)
       auto part = [&]() -> size_t {
         if constexpr (!kFp4) return ((size_t)t * p.n_slots + (w + s.b)) * kHeads + kHalfHeads * rank + hl;
         return ((size_t)row_t * p.n_slots + (w + s.b)) * n_heads + (row - row_t * n_heads);
@@ -944,7 +944,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
       const float l_tot = l_part + red_l[(half ^ 1) * 64 + hl];
       asm volatile("bar.sync 1, 128;" ::: "memory");
       const float inv = l_tot > 0.f ? 1.f / l_tot : 0.f;
-      // O leaves, normalised and rounded to bf16, through the (free) P buffer
+      // O leaves, normalised and rounded to bf16 (4-bit cache: to f16, whose range
+      // the latent keeps here anyway: the partials' rounding is 2^-12, not 2^-9, for
+      // the same bytes), through the (free) P buffer
       // as 64-column x 64-head boxes stored by TMA: lanes 0-63 hold dims
       // [256j, 256j+128), lanes 64-127 dims [256j+128, 256j+256).  Four 8 KB
       // staging slots: two iterations of both halves in flight.
@@ -973,9 +975,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kCache>::Th
             uint32_t u[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 v2 = __floats2bfloat162_rn(__uint_as_float(orr[8 * q + 2 * e]) * inv,
-                                                              __uint_as_float(orr[8 * q + 2 * e + 1]) * inv);
-              u[e] = *reinterpret_cast<const uint32_t*>(&v2);
+              const float v0 = __uint_as_float(orr[8 * q + 2 * e]) * inv, v1 = __uint_as_float(orr[8 * q + 2 * e + 1]) * inv;
+              if constexpr (kFp4) {
+                const __half2 v2 = __floats2half2_rn(v0, v1);
+                u[e] = *reinterpret_cast<const uint32_t*>(&v2);
+              } else {
+                const __nv_bfloat162 v2 = __floats2bfloat162_rn(v0, v1);
+                u[e] = *reinterpret_cast<const uint32_t*>(&v2);
+              }
             }
             if (boxes)
               *reinterpret_cast<uint4*>(box + ((q ^ (hl & 7)) * 16)) = make_uint4(u[0], u[1], u[2], u[3]);

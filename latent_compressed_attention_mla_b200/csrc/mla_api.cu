@@ -233,13 +233,15 @@ int mla_combine(const mla_dims* dims, const void* W_uv, int batch, int n_q, int 
   if (!workspace || ws_bytes < L.total) return MLA_ERR_WORKSPACE;
   if (!aligned16(W_uv) || !aligned16(workspace)) return MLA_ERR_ALIGNMENT;
   const uint8_t* ws = static_cast<const uint8_t*>(workspace);
-  // the partials' row type follows the decode path that wrote them; the kernel
-  // that reads bf16 rows stores pairs
-  const bool part_bf16 = mla_decode_path(dims, n_q) >= 1;
-  if (part_bf16 && (reinterpret_cast<uintptr_t>(out) & 3u)) return MLA_ERR_ALIGNMENT;
+  // the partials' row type follows the decode path that wrote them; the combine
+  // that reads a tensor-core decode's stores pairs
+  const int path = mla_decode_path(dims, n_q);
+  const bool fp4 = path >= 1 && dims->cache_dtype == MLA_FP4_E2M1;
+  const PartType part = path < 1 || path == 2 ? kPartF32 : fp4 ? kPartF16 : kPartBf16;
+  if (path >= 1 && (reinterpret_cast<uintptr_t>(out) & 3u)) return MLA_ERR_ALIGNMENT;
   trace_record(MLA_TRACE_COMBINE, false, (cudaStream_t)stream);
   cudaError_t e = launch_combine(*dims, W_uv, batch, n_q, reinterpret_cast<const int32_t*>(ws + L.off_plan),
-                                 reinterpret_cast<const float*>(ws + L.off_o), part_bf16,
+                                 reinterpret_cast<const float*>(ws + L.off_o), part, fp4,
                                  reinterpret_cast<const float*>(ws + L.off_lse), out, lse_out, status_ptr(),
                                  (cudaStream_t)stream);
   trace_record(MLA_TRACE_COMBINE, true, (cudaStream_t)stream);

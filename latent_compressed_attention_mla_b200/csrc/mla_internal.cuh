@@ -254,9 +254,9 @@ __device__ __forceinline__ void rope_cos_sin(int pos, int i, int half, float bas
 //           overlapping each sequence
 //   q_abs : [batch, n_q, n_heads, d_c + d_rope] act type (absorbed queries,
 //           rotated q^R appended)
-//   o_part: [n_q, n_slots, n_heads, d_c] per-split normalised latent sums,
-//           float32 rows from the CUDA-core decode, bf16 rows (in the first
-//           half of the region) from the tensor-core decode
+//   o_part: [n_q, n_slots, n_heads, d_c] per-split normalised latent sums in
+//           rows of the decode kernel's PartType (16-bit rows in the first half
+//           of the region)
 //   lse   : float32 [n_q, n_slots, n_heads] per-split log2-sum-exp2 of the scores
 //           scaled by softmax_scale*log2(e) (-inf for an empty split)
 // A split w covers global key tiles [w*TT/W, (w+1)*TT/W) of the concatenated
@@ -435,10 +435,13 @@ int decode_few_auto_splits(int num_sms);
 cudaError_t launch_decode_few(const DecodeParams& p, cudaStream_t st);
 int decode_tc_auto_splits(const mla_dims& d, int num_sms, int n_q);
 
-// part_bf16: the split partials are bf16 rows (the tensor-core decode writes
-// them so), else fp32 (the CUDA-core decode)
+// The split partials' rows as the decode kernels write them: fp32 (CUDA cores;
+// warp-level MMA over a 4-bit cache), bf16 (tcgen05, bf16 and FP8 caches), f16
+// (tcgen05, 4-bit cache).  two_terms: the combine's product takes the merged
+// latent sum as two bf16 terms, not one rounded to bf16.
+enum PartType { kPartF32 = 0, kPartBf16 = 1, kPartF16 = 2 };
 cudaError_t launch_combine(const mla_dims& d, const void* W_uv, int batch, int n_q, const int32_t* plan,
-                           const float* o_part, bool part_bf16, const float* lse_part, void* out, float* lse_out,
+                           const float* o_part, PartType part, bool two_terms, const float* lse_part, void* out, float* lse_out,
                            int* status, cudaStream_t st);
 
 }  // namespace mla
