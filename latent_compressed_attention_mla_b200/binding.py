@@ -131,6 +131,15 @@ def _cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors passed to libmla must be contiguous CUDA tensors")
+    _on_current_device(*ts)
+
+
+def _on_current_device(*ts):
+    """The kernels run on the current device, with whose memory alone they work."""
+    here = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor on cuda:{t.get_device()} while the current device is cuda:{here}")
 
 
 def cache_page_bytes(dims: MlaDims) -> int:
@@ -190,16 +199,19 @@ def _rows(x, n, width, dtype, what):
     """Row stride (elements) of an [n, width] CUDA tensor with contiguous rows."""
     if tuple(x.shape) != (n, width) or x.dtype != dtype or not x.is_cuda:
         raise ValueError(f"{what}: a CUDA tensor [{n}, {width}] of {dtype}")
+    _on_current_device(x)
     step, unit = x.stride()
     if unit != 1 and width > 1 and n > 0:
         raise ValueError(f"{what}: rows must be contiguous")
     return step if n > 1 else max(step, width)
 
 
-def _index(n, *ts):
+def _index(n, page_table, *ts):
     for t in ts:
         if t.dtype != torch.int32 or t.numel() != n:
             raise ValueError("seq_idx and pos: one int32 per row")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table: int32 [batch, max_pages]")
 
 
 def act_dtype(dims: MlaDims):
@@ -217,7 +229,7 @@ def mla_append_rows(dims, c, k_rope, seq_idx, pos, page_table, cache_pool, norm_
     cs, ks = _rows(c, n, dims.d_c, act, "c"), _rows(k_rope, n, dims.d_rope, act, "k_rope")
     if norm_weight is not None and (norm_weight.dtype != act or norm_weight.numel() != dims.d_c):
         raise ValueError(f"norm_weight: [d_c] of {act}")
-    _index(n, seq_idx, pos)
+    _index(n, page_table, seq_idx, pos)
     num_pages = cache_pool.numel() * cache_pool.element_size() // cache_page_bytes(dims)
     rc = lib().mla_append_rows(ctypes.byref(dims), _ptr(c), cs, _ptr(k_rope), ks, _ptr(norm_weight), norm_eps, n,
                                _ptr(seq_idx), _ptr(pos), _ptr(page_table), page_table.shape[0], page_table.shape[1],
@@ -232,7 +244,7 @@ def mla_read_rows(dims, cache_pool, page_table, seq_idx, pos, c_out, k_out, stre
     if tuple(c_out.shape) != (n, dims.d_c) or tuple(k_out.shape) != (n, dims.d_rope) or c_out.dtype != act or \
             k_out.dtype != act:
         raise ValueError(f"c_out [N, d_c], k_out [N, d_rope]: {act}")
-    _index(n, seq_idx, pos)
+    _index(n, page_table, seq_idx, pos)
     num_pages = cache_pool.numel() * cache_pool.element_size() // cache_page_bytes(dims)
     rc = lib().mla_read_rows(ctypes.byref(dims), _ptr(cache_pool), num_pages, _ptr(page_table), page_table.shape[0],
                              page_table.shape[1], _ptr(seq_idx), _ptr(pos), n, _ptr(c_out), _ptr(k_out),

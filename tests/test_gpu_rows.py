@@ -354,3 +354,74 @@ def test_append_latent_into_a_4bit_cache(n, entry):
     assert np.all(np.abs(gc - c) <= step * (1 + 1e-6) + err)
     assert (O.fp4_dequantise_latent(codes, s, ts) != gc).mean() < 1e-3  # all but border cases agree exactly
     assert np.all(np.abs(gk - kr) <= 2.0 ** -8 * np.abs(kr) + 4 * err)
+
+
+MANY = 19_001  # read_rows takes four tokens a warp and append_rows' warps loop
+
+
+@pytest.mark.parametrize("odd_out", [False, True])
+@pytest.mark.parametrize("act,cache", TYPES)
+def test_many_rows_in_one_call_are_the_rows_of_many_calls(act, cache, odd_out):
+    """Bad slots among them: those write nothing, and their outputs stay as they were."""
+    r = Rows(act, cache, MANY, d_c=256, d_rope=64, batch=4)
+    bad = np.array([0, 1, 777, 4_000, 4_003, 12_345, MANY - 1])
+    r.pos[torch.from_numpy(bad)] = torch.tensor([-1, 10 ** 9, -5, 10 ** 6, -1, 10 ** 8, -1], dtype=torch.int32)
+    c, kr, seq, pos, table = r.cuda()
+    r.cache.append(c, kr, seq, pos, table, r.w.cuda())
+    assert B.mla_get_status() == B.MLA_ERR_BOUNDS
+    one = r.cache.pool.clone()
+    r.cache.pool.fill_(0xA5)
+    for i in range(0, MANY, 3_000):
+        j = min(i + 3_000, MANY)
+        r.cache.append(c[i:j], kr[i:j], seq[i:j].contiguous(), pos[i:j].contiguous(), table, r.w.cuda())
+    assert torch.equal(one, r.cache.pool)
+
+    def out(width):
+        flat = torch.full((MANY * width + 1,), 3.0, dtype=r.dt, device="cuda")
+        return (flat[1:] if odd_out else flat[:-1]).view(MANY, width)
+
+    co, ko = out(256), out(64)
+    B.mla_read_rows(r.dims, r.cache.pool, table, seq, pos, co, ko)
+    cs, ks = torch.full_like(co, 3.0), torch.full_like(ko, 3.0)
+    for i in range(0, MANY, 3_000):
+        j = min(i + 3_000, MANY)
+        B.mla_read_rows(r.dims, r.cache.pool, table, seq[i:j].contiguous(), pos[i:j].contiguous(), cs[i:j], ks[i:j])
+    torch.cuda.synchronize()
+    assert torch.equal(co, cs) and torch.equal(ko, ks)
+    assert (co[bad] == 3.0).all() and (ko[bad] == 3.0).all()
+    good = np.setdiff1d(np.arange(MANY), bad)
+    assert (co[good].float().abs().sum(1) > 0).all()
+    assert B.mla_get_status() == B.MLA_ERR_BOUNDS
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp4"])
+def test_append_and_read_captured_and_replayed_beside_another_stream(cache):
+    """One graph of an append and a read, replayed with new inputs while a second stream reads another pool."""
+    a, b = Rows("bf16", cache, 300, seed=3), Rows("bf16", cache, 300, seed=4)
+    a.append(norm=True)
+    b.append(norm=True)
+    c, kr, seq, pos, table = a.cuda()
+    w = a.w.cuda()
+    c, kr = c.contiguous(), kr.contiguous()
+    co, ko = torch.empty_like(c), torch.empty_like(kr)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.cache.append(c, kr, seq, pos, table, w)
+        B.mla_read_rows(a.dims, a.cache.pool, table, seq, pos, co, ko)
+    _, _, seq_b, pos_b, table_b = b.cuda()
+    want_b = b.cache.values(seq_b, pos_b, table_b)
+    torch.cuda.synchronize()
+    for k in range(3):
+        c.mul_(-1.5)
+        torch.cuda.synchronize()
+        g.replay()
+        with torch.cuda.stream(side):
+            got_b = b.cache.values(seq_b, pos_b, table_b)
+        torch.cuda.synchronize()
+        fresh = Rows("bf16", cache, 300, seed=3)
+        fresh.cache.append(c, kr, seq, pos, table, w)
+        want = fresh.cache.values(seq, pos, table)
+        torch.cuda.synchronize()
+        assert torch.equal(co, want[0]) and torch.equal(ko, want[1])
+        assert torch.equal(got_b[0], want_b[0]) and torch.equal(got_b[1], want_b[1])

@@ -125,3 +125,30 @@ def test_few_heads_have_a_workspace_size(heads, cache):
     d = B.make_dims(heads, 512, 64, 128, 128, 7168, cache=cache)
     assert B.auto_splits(d, 1, 1) >= 1
     assert B.decode_workspace_bytes(d, 2, 1, 0) > 0
+
+
+def test_binding_refuses_another_device_and_other_index_types(monkeypatch):
+    class OnDevice:
+        is_cuda = True
+
+        def __init__(self, index):
+            self.index = index
+
+        def is_contiguous(self):
+            return True
+
+        def get_device(self):
+            return self.index
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    B._cuda(OnDevice(0), None)
+    with pytest.raises(ValueError, match="cuda:1"):
+        B._cuda(OnDevice(0), OnDevice(1))
+    i32 = torch.zeros(4, dtype=torch.int32)
+    B._index(4, i32.view(2, 2), i32, i32)
+    with pytest.raises(ValueError, match="page_table"):
+        B._index(4, i32.view(2, 2).long(), i32, i32)
+    with pytest.raises(ValueError, match="page_table"):
+        B._index(4, i32, i32, i32)
+    with pytest.raises(ValueError, match="int32"):
+        B._index(4, i32.view(2, 2), i32, i32.long())
