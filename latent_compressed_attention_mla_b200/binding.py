@@ -112,13 +112,17 @@ def dims_for(cfg, flags: int = 0) -> MlaDims:
 
 # (Plain integers pass as c_void_p arguments; making a c_void_p, or a
 # torch.cuda.Stream object for the current stream, costs microseconds a call.)
+def _device():
+    return torch._C._cuda_getDevice()
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_device())
     return stream.cuda_stream
 
 
@@ -128,18 +132,25 @@ def _check(rc: int, what: str):
 
 
 def _cuda(*ts):
+    """Contiguous CUDA tensors of the current device, on which the kernels run; returns it."""
+    here = -1
     for t in ts:
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
+        if t is None:
+            continue
+        if here < 0 or t.get_device() != here:
+            here = _on_current_device(t)
+        if not t.is_contiguous():
             raise ValueError("tensors passed to libmla must be contiguous CUDA tensors")
-    _on_current_device(*ts)
+    return here
 
 
-def _on_current_device(*ts):
-    """The kernels run on the current device, with whose memory alone they work."""
-    here = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor on cuda:{t.get_device()} while the current device is cuda:{here}")
+def _on_current_device(t):
+    at = t.get_device()
+    if at < 0:
+        raise ValueError("tensors passed to libmla must be contiguous CUDA tensors")
+    if at != _device():
+        raise ValueError(f"a tensor on cuda:{at} while the current device is cuda:{_device()}")
+    return at
 
 
 def cache_page_bytes(dims: MlaDims) -> int:
@@ -195,11 +206,12 @@ def mla_append_latent_noalloc(dims, h, seq_idx, pos, W_dkv, W_kr, page_table, ca
     _check(rc, "mla_append_latent_noalloc")
 
 
-def _rows(x, n, width, dtype, what):
+def _rows(x, n, width, dtype, what, here):
     """Row stride (elements) of an [n, width] CUDA tensor with contiguous rows."""
     if tuple(x.shape) != (n, width) or x.dtype != dtype or not x.is_cuda:
         raise ValueError(f"{what}: a CUDA tensor [{n}, {width}] of {dtype}")
-    _on_current_device(x)
+    if x.get_device() != here:
+        _on_current_device(x)
     step, unit = x.stride()
     if unit != 1 and width > 1 and n > 0:
         raise ValueError(f"{what}: rows must be contiguous")
@@ -224,9 +236,9 @@ def mla_append_rows(dims, c, k_rope, seq_idx, pos, page_table, cache_pool, norm_
     if given) and k_rope [N, d_rope] (not rotated), both views with contiguous
     rows (a slice of a fused projection's output serves), go to
     (seq_idx[n], pos[n]) of the paged cache."""
-    _cuda(seq_idx, pos, page_table, cache_pool, norm_weight)
+    here = _cuda(seq_idx, pos, page_table, cache_pool, norm_weight)
     n, act = c.shape[0], act_dtype(dims)
-    cs, ks = _rows(c, n, dims.d_c, act, "c"), _rows(k_rope, n, dims.d_rope, act, "k_rope")
+    cs, ks = _rows(c, n, dims.d_c, act, "c", here), _rows(k_rope, n, dims.d_rope, act, "k_rope", here)
     if norm_weight is not None and (norm_weight.dtype != act or norm_weight.numel() != dims.d_c):
         raise ValueError(f"norm_weight: [d_c] of {act}")
     _index(n, page_table, seq_idx, pos)

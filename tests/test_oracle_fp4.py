@@ -129,8 +129,6 @@ def test_few_heads_have_a_workspace_size(heads, cache):
 
 def test_binding_refuses_another_device_and_other_index_types(monkeypatch):
     class OnDevice:
-        is_cuda = True
-
         def __init__(self, index):
             self.index = index
 
@@ -140,7 +138,7 @@ def test_binding_refuses_another_device_and_other_index_types(monkeypatch):
         def get_device(self):
             return self.index
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(B, "_device", lambda: 0)
     B._cuda(OnDevice(0), None)
     with pytest.raises(ValueError, match="cuda:1"):
         B._cuda(OnDevice(0), OnDevice(1))
