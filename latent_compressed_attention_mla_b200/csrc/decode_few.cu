@@ -36,6 +36,15 @@
 // A warp interleaves the scores of tile i + 1 with the values of tile i: two
 // independent streams of conversions and MMAs (two warps a scheduler are too
 // few to hide one stream's latencies; P is double-buffered).
+//
+// Measured (16 heads): 128 sequences of 16,385 keys 377 us, 2.4 TB/s of cache rows;
+// 8 of 131,073 202 us.  HBM would allow 135 and 68; loads alone take 148.  Bound by
+// the math pipes: each code becomes f16 twice (scores, values), and per 128 keys a
+// scheduler issues 272 MMAs (8.6 cycles each), 512 conversions of two codes (2) and
+// 512 multiplies.  Twice the warps do not help: sixteen with half the work each
+// 382 us, two teams of eight on alternate pages, one's softmax beside the other's
+// products, 394 us.  On the way: one phase for scores, one for values 499 us; query
+// fragments in registers, not shared memory 412 us.
 #include <cuda.h>
 
 #include <cstring>
