@@ -41,7 +41,7 @@ L2_BYTES = 126 * 1024 * 1024
 # kernel (bench name) -> sources whose content decides its DRAM counters
 KERNEL_SOURCES = {
     "append_project": ["csrc/append.cu"], "append_finalize": ["csrc/append.cu"], "absorb": ["csrc/absorb.cu"],
-    "attend": ["csrc/decode_tc.cu", "csrc/decode_simt.cu"], "combine": ["csrc/combine.cu"],
+    "attend": ["csrc/decode_tc.cu", "csrc/decode_tc.cuh", "csrc/decode_simt.cu"], "combine": ["csrc/combine.cu"],
 }
 COMMON_SOURCES = ["csrc/mla_internal.cuh", "csrc/mma_tile.cuh", "csrc/tensor_map.cu"]
 

@@ -429,6 +429,7 @@ __device__ __forceinline__ void mla_stamp_now(int e) {
 #define MLA_STAMP_EXPORT(unit)
 #endif
 cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t st);
+cudaError_t launch_decode_tc_fp4(const DecodeParams& p, cudaStream_t st);
 // few query rows over a 4-bit cache, warp-level tensor cores (decode_few.cu)
 bool decode_few_supported(const mla_dims& d, int n_q);
 int decode_few_auto_splits(int num_sms);
