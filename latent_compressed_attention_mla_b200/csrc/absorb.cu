@@ -499,8 +499,8 @@ bool absorb_tc_fits(const mla_dims& d) { return d.d_nope == kTcDn && d.d_c == kT
 
 cudaError_t launch_absorb_and_plan(const mla_dims& d, const void* q_nope, const void* q_rope, const void* W_uk,
                                    const int32_t* seq_lens, int batch, int n_q, int max_pages, int splits,
-                                   void* q_abs, bool q_abs_f16, bool q_rope_bf16, int32_t* plan, float* lse_part, size_t lse_count,
-                                   int* status, cudaStream_t st) {
+                                   void* q_abs, bool q_abs_f16, bool q_rope_bf16, int32_t* plan, float* lse_part,
+                                   size_t lse_count, int* status, cudaStream_t st) {
   AbsorbArgs a;
   a.q_nope = q_nope;
   a.q_rope = q_rope;

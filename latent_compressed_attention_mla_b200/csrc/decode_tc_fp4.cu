@@ -257,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L::Threads, 1)
         return ((size_t)row_t * p.n_slots + (w + s.b)) * n_heads + (row - row_t * n_heads);
       };
       if (s.n_pages == 0 || !ok) {
-        __nv_bfloat16* od = reinterpret_cast<__nv_bfloat16*>(p.o_part) + part() * kDC;
+        __half* od = reinterpret_cast<__half*>(p.o_part) + part() * kDC;
         if (row_ok) {
           for (int j = 0; j < 2; ++j)
             for (int c = 0; c < 128; c += 8)
@@ -453,8 +453,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L::Threads, 1)
             if (boxes)
               *reinterpret_cast<uint4*>(box + ((q ^ (hl & 7)) * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
             else if (row_ok)
-              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o_part) + part() * kDC + (c < 128 ? 0 : 256) + 128 * half + (c & 127) + 8 * q) =
-                  make_uint4(u[0], u[1], u[2], u[3]);
+              *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(p.o_part) + part() * kDC + (c < 128 ? 0 : 256) +
+                                        128 * half + (c & 127) + 8 * q) = make_uint4(u[0], u[1], u[2], u[3]);
           }
           fence_proxy_async();
           asm volatile("bar.sync %0, 64;" ::"r"(2 + half) : "memory");
