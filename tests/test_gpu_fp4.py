@@ -304,3 +304,46 @@ def test_combine_refuses_an_output_that_holds_no_pairs(cache, heads):
     with pytest.raises(B.MlaError, match="ALIGN"):
         B.mla_combine(gp.dims, gp.weights["W_uv"], 1, 1, ws, odd.view(out.shape))
     assert odd.abs().sum().item() == 0 and gp.status() == 0
+
+
+@pytest.mark.parametrize("heads", [8, 40, 128])
+def test_captured_graphs_replayed_on_two_streams(heads):
+    """Two graphs of decode and combine, each with its workspace, replayed side by side with new queries and
+    lengths, give what eager calls give."""
+    runs = []
+    for k in range(2):
+        cfg = fp4_cfg(B=3, T=1, L=(5, 700, 131), n_heads=heads, seed=21 + k)
+        gp = GpuProblem(cfg)
+        gp.session.append(gp.inputs["h"], gp.seq_idx, gp.pos, gp.weights["W_dkv"], gp.weights["W_kr"], gp.page_table,
+                          gp.cache.pool)
+        ws = torch.empty(B.decode_workspace_bytes(gp.dims, 3, 1), dtype=torch.uint8, device="cuda")
+        q_nope, q_rope = gp.inputs["q_nope"].clone(), gp.inputs["q_rope"].clone()
+        lens = torch.from_numpy(cfg.seq_lens.astype(np.int32)).cuda()
+        out = torch.empty(3, 1, heads, cfg.d_v, dtype=torch.bfloat16, device="cuda")
+
+        def step(gp=gp, ws=ws, q_nope=q_nope, q_rope=q_rope, lens=lens, out=out):
+            B.mla_decode(gp.dims, q_nope, q_rope, gp.weights["W_uk"], gp.cache.pool, gp.page_table, lens, ws)
+            B.mla_combine(gp.dims, gp.weights["W_uv"], 3, 1, ws, out)
+
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        runs.append((g, step, q_nope, lens, out, torch.cuda.Stream()))
+    for _ in range(3):
+        for _, _, q_nope, lens, _, _ in runs:
+            q_nope.mul_(-0.75)
+            lens.sub_(1)
+        torch.cuda.synchronize()
+        for g, _, _, _, _, s in runs:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        got = [r[4].clone() for r in runs]
+        for r, want in zip(runs, got):
+            r[4].zero_()
+            r[1]()
+            torch.cuda.synchronize()
+            assert torch.equal(r[4], want) and want.abs().sum().item() > 0
+    assert B.mla_get_status() == 0
