@@ -263,6 +263,8 @@ int mla_read_rows(const mla_dims* dims, const void* cache_pool, int num_pages,
  * probabilities as f16, and all but the few-row kernel (path 2) the latent too:
  * |q~| and |c| up to 65504, and where a token's largest |c| is below 2^-15 its
  * small elements lose bits (absolute error up to 2^-25).
+ * A visible row that is not finite makes the query's scores and results NaN
+ * (out and lse_out of mla_combine), whatever the splits.
  * The workspace is consumed by the next mla_combine with the same dims, batch,
  * n_q and num_splits.
  * ------------------------------------------------------------------------- */

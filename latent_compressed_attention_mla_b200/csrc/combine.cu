@@ -82,21 +82,22 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(
       for (int k = lane; k < n; k += 32) mx = fmaxf(mx, lse[(size_t)k * n_heads]);
 #pragma unroll
       for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (mx == -INFINITY) mx = 0.f;  // no split holds a key with a finite score: weights 0, or NaN
       float sum = 0.f;
       for (int k = lane; k < n; k += 32) {
-        const float e = mx > -INFINITY ? exp2f(lse[(size_t)k * n_heads] - mx) : 0.f;
+        const float e = exp2f(lse[(size_t)k * n_heads] - mx);
         wgt[warp * kMaxSplits + k] = e;
         sum += e;
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       __syncwarp();
       for (int k = lane; k < n; k += 32) wgt[warp * kMaxSplits + k] *= inv;
       if (lane == 0) {
         s_lo[warp] = lo;
         s_n[warp] = n;
-        if (lse_out) lse_out[(size_t)m * n_heads + h] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+        if (lse_out) lse_out[(size_t)m * n_heads + h] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
       }
     }
     __syncthreads();
@@ -304,18 +305,21 @@ __global__ void __launch_bounds__(kThreads) combine_tc_kernel(const __grid_const
         for (int k = lane + 32; k < n; k += 32) mx = fmaxf(mx, lse[(size_t)k * n_heads]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        // a split holding no key of the sequence has lse = -inf: weight 0
-        const float e = mx > -INFINITY ? exp2f(lv[j] - mx) : 0.f;
+        // a split holding no key of the sequence has lse = -inf: weight 0; one
+        // with a visible key that is not finite has lse = NaN, which the sum
+        // and with it every weight of the row take on
+        if (mx == -INFINITY) mx = 0.f;
+        const float e = exp2f(lv[j] - mx);
         float sum = e;
         for (int k = lane + 32; k < n; k += 32) sum += exp2f(lse[(size_t)k * n_heads] - mx);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         s_w[mi][lane] = e * inv;
         if (lane == 0) {
           s_mx[mi] = mx;
           s_inv[mi] = inv;
-          if (P.lse_out && mi < mc) P.lse_out[(size_t)(m0 + mi) * n_heads + h] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+          if (P.lse_out && mi < mc) P.lse_out[(size_t)(m0 + mi) * n_heads + h] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
         }
       }
     }

@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_few_kernel(const __grid_co
             for (int j = 0; j < 8; j += 4)
               dst[2 * c + j / 4] = make_float4(o[j][2 * r + c] * inv, o[j + 1][2 * r + c] * inv, o[j + 2][2 * r + c] * inv,
                                                o[j + 3][2 * r + c] * inv);
-          if (ds == 0 && q == 0) p.lse_part[part] = l[r] > 0.f ? m_ref[r] + __log2f(l[r]) : -INFINITY;
+          if (ds == 0 && q == 0) p.lse_part[part] = l[r] == 0.f ? -INFINITY : m_ref[r] + __log2f(l[r]);
         }
       }
       sync_warps();  // s_l is rewritten by the next piece

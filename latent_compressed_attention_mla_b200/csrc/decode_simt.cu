@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeParams p) {
 #pragma unroll
     for (int j = 0; j < kMaxOutPerThread; ++j)
       if (j < n_out) od[kl + TPH * j] = o[j] * inv_l;
-    if (kl == 0) p.lse_part[slot * p.d.n_heads + h] = l > 0.f ? m + log2f(l) : -INFINITY;
+    if (kl == 0) p.lse_part[slot * p.d.n_heads + h] = l == 0.f ? -INFINITY : m + log2f(l);
     g = seg_end;
   }
   tl_end(p.timeline, MLA_TRACE_ATTEND);

@@ -980,7 +980,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcLayout<kFp8>::Thre
         if (issuer) bulk_wait_all();
         asm volatile("bar.sync %0, 64;" ::"r"(2 + half) : "memory");
       }
-      if (half == 0) p.lse_part[slot * kHeads + head] = l_tot > 0.f ? m_ref + __log2f(l_tot) : -INFINITY;
+      if (half == 0) p.lse_part[slot * kHeads + head] = l_tot == 0.f ? -INFINITY : m_ref + __log2f(l_tot);
       if (threadIdx.x == 0) TC_TRACE(15, 0);
       MLA_STAMP(2);
       tc_fence_before();

@@ -469,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L::Threads, 1)
         if (issuer) bulk_wait_all();
         asm volatile("bar.sync %0, 64;" ::"r"(2 + half) : "memory");
       }
-      if (half == 0 && row_ok) p.lse_part[part()] = l_tot > 0.f ? m_ref + __log2f(l_tot) : -INFINITY;
+      if (half == 0 && row_ok) p.lse_part[part()] = l_tot == 0.f ? -INFINITY : m_ref + __log2f(l_tot);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(leader_bar(L::O_FREE));

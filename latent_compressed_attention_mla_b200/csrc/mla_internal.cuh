@@ -258,7 +258,8 @@ __device__ __forceinline__ void rope_cos_sin(int pos, int i, int half, float bas
 //           rows of the decode kernel's PartType (16-bit rows in the first half
 //           of the region)
 //   lse   : float32 [n_q, n_slots, n_heads] per-split log2-sum-exp2 of the scores
-//           scaled by softmax_scale*log2(e) (-inf for an empty split)
+//           scaled by softmax_scale*log2(e) (-inf for an empty split, NaN for one
+//           with a visible key whose score is NaN)
 // A split w covers global key tiles [w*TT/W, (w+1)*TT/W) of the concatenated
 // sequences; its piece of sequence b goes to slot w + b (n_slots = batch + W - 1).
 // ----------------------------------------------------------------------------

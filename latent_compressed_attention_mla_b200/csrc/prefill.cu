@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kTThreads, 1) prefill_attn_tc_kernel(const __g
             *reinterpret_cast<uint4*>(orow + 32 * c + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
       }
       if (half == 0 && a.lse_out && t < T)
-        a.lse_out[((size_t)b * T + t) * H + h] = lt > 0.f ? (m + log2f(lt)) * kLn2 : -INFINITY;
+        a.lse_out[((size_t)b * T + t) * H + h] = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
     }
   }
 

@@ -1,0 +1,71 @@
+"""Rows of the cache that are not finite.  A query that sees such a row answers
+NaN (output and log-sum-exp), whatever the number of splits; every other query's
+result is the one without it, bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+from latent_compressed_attention_mla_b200 import binding as B
+from latent_compressed_attention_mla_b200 import workloads as W
+from tests.gpu_harness import GpuProblem
+
+pytestmark = pytest.mark.gpu
+
+# (cache type, heads, flags); f32: the tiny dims with fp32 activations
+DECODES = [("f32", 4, 0), ("bf16", 16, 0), ("bf16", 128, 0), ("fp8", 128, 0), ("fp4", 8, 0), ("fp4", 40, 0),
+           ("fp4", 64, 0), ("fp4", 128, 0), ("fp4", 16, B.MLA_FLAG_FORCE_SIMT)]
+IDS = [f"{c}-h{h}" + ("-simt" if f else "") for c, h, f in DECODES]
+
+
+def make(cache, heads, flags, T, L, splits=0):
+    base = W.TINY_F32 if cache == "f32" else W.V3_FP8_B128_T2.with_(cache_dtype=cache)
+    cfg = base.with_(n_heads=heads, B=len(L), T=T, L=tuple(L), name=f"nonfinite-{cache}-{heads}")
+    return cfg, GpuProblem(cfg, flags=flags, num_splits=splits)
+
+
+def overwrite(gp, b, pos, value, where):
+    """Row (b, pos) anew through the append of projected rows, with one element
+    of c ("c") or of k^R ("kr") that is not finite."""
+    d = gp.dims
+    act = B.act_dtype(d)
+    c = W.normal(31, 1, d.d_c).view(1, -1).to(act).cuda()
+    kr = W.normal(31, 2, d.d_rope).view(1, -1).to(act).cuda()
+    (c if where == "c" else kr)[0, 7] = value
+    at = torch.tensor([b], dtype=torch.int32, device="cuda"), torch.tensor([pos], dtype=torch.int32, device="cuda")
+    gp.cache.append(c, kr, *at, gp.page_table)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 7])
+@pytest.mark.parametrize("cache,heads,flags", DECODES, ids=IDS)
+def test_a_visible_row_makes_its_sequence_nan(cache, heads, flags, splits):
+    cfg, gp = make(cache, heads, flags, 2, (300, 3000, 65), splits)
+    out, lse = gp.run()
+    ref, ref_lse = out.clone(), lse.clone()
+    overwrite(gp, 1, 1777, float("nan"), "c")
+    out, lse = gp.attend_only()
+    for b in (0, 2):
+        assert torch.equal(out[b], ref[b]) and torch.equal(lse[b], ref_lse[b])
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    assert torch.isfinite(ref.float()).all() and gp.status() == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp4"])
+def test_a_visible_row_makes_the_prefill_nan(cache):
+    cfg, gp = make(cache, 2, 0, 100, (130,))
+    append(gp)
+    overwrite(gp, 0, 77, float("nan"), "c")
+    out, lse = prefill(cfg, gp)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+def append(gp):
+    gp.session.append(gp.inputs["h"], gp.seq_idx, gp.pos, gp.weights["W_dkv"], gp.weights["W_kr"], gp.page_table,
+                      gp.cache.pool)
+
+
+def prefill(cfg, gp):
+    i = gp.inputs
+    out, lse = gp.session.prefill(i["q_nope"], i["q_rope"], gp.weights["W_uk"], gp.weights["W_uv"], gp.cache.pool,
+                                  gp.page_table, gp.seq_lens, int(cfg.seq_lens.max()))
+    torch.cuda.synchronize()
+    return out.clone(), lse.clone()
