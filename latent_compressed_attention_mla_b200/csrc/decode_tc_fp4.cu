@@ -99,10 +99,12 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 
 // 32 e2m1 codes (two blocks of 16 columns) times their scales -> 64 bytes of
 // f16: the 16-byte units u0 ^ e, e = 0..3, of a 128-byte swizzled row.  sc: the
-// blocks' e4m3 scales (low byte first); ts: the token's scale, twice.
-__device__ __forceinline__ void store_e2m1x32(uint8_t* row, uint32_t u0, const uint4& w, uint32_t sc, uint32_t ts) {
+// blocks' e4m3 scales (low byte first); nan: the f16 pair that a NaN scale
+// becomes (scales are not negative); ts: the token's scale, twice.
+__device__ __forceinline__ void store_e2m1x32(uint8_t* row, uint32_t u0, const uint4& w, uint32_t sc, uint32_t nan,
+                                              uint32_t ts) {
   const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-  const uint32_t s = mul_f16x2(e4m3x2_to_f16x2(sc), ts), s0 = dup_lo(s), s1 = dup_hi(s);
+  const uint32_t s = mul_f16x2(max_f16x2(e4m3x2_to_f16x2(sc), nan), ts), s0 = dup_lo(s), s1 = dup_hi(s);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t r[4];
@@ -500,6 +502,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L::Threads, 1)
     // staged codes: 16-byte piece 2 x + q of a 64-byte row, x the unit (QK) or
     // the half (PV); 4096-byte box the half (QK) or the unit (PV)
     const uint32_t x0 = (uint32_t)(q ^ ((row >> 1) & 3)) << 4, x1 = x0 ^ 32u;
+    // A NaN scale stays one in the scores, which is how the rows that see the key
+    // get it, and counts as 0 among the values: there a row of the group whose
+    // causal limit hides the key would take 0 times NaN.
+    const uint32_t nan = pv ? 0u : 0x7FFF7FFFu;
     // the two 8-byte groups of block scales: the halves' pages (QK), the units' columns (PV)
     const uint32_t scl_g = pv ? 16 : L::PageScl, ts_a = pv ? 0 : L::PageScl;
     RingPos unit, stage;
@@ -557,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L::Threads, 1)
             if (!ok) break;
             uint8_t* const dst = ring + unit.slot * kUnitBytes;
 #pragma unroll
-            for (int a = 0; a < 2; ++a) store_e2m1x32(dst + a * 8192, u0, v[a], sc[a] >> (16 * q), ts[a]);
+            for (int a = 0; a < 2; ++a) store_e2m1x32(dst + a * 8192, u0, v[a], sc[a] >> (16 * q), nan, ts[a]);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(un_full + 8 * unit.slot);

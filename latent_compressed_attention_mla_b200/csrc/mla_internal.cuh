@@ -211,6 +211,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// the larger of each two; of a NaN and a number the number
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 // two e4m3 codes (low byte first) as an f16 pair
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t s) {
   uint32_t d;

@@ -69,3 +69,22 @@ def prefill(cfg, gp):
                                   gp.page_table, gp.seq_lens, int(cfg.seq_lens.max()))
     torch.cuda.synchronize()
     return out.clone(), lse.clone()
+
+
+@pytest.mark.parametrize("where,value", [("c", float("nan")), ("c", float("inf")), ("kr", float("nan"))])
+@pytest.mark.parametrize("T", [2, 3])
+@pytest.mark.parametrize("cache,heads,flags", DECODES, ids=IDS)
+def test_a_hidden_row_does_not_reach_earlier_queries(cache, heads, flags, T, where, value):
+    """The last of the new tokens is not finite: the queries before it do not see it
+    (it is alone in its page, or in its tile of pages, in some of the sequences)."""
+    cfg, gp = make(cache, heads, flags, T, (63 - T, 700, 2, 65 - T, 129 - T, 257 - T))
+    out, lse = gp.run()
+    ref, ref_lse = out.clone(), lse.clone()
+    for b in range(cfg.B):
+        overwrite(gp, b, int(cfg.seq_lens[b]) - 1, value, where)
+    out, lse = gp.attend_only()
+    assert torch.equal(out[:, :-1], ref[:, :-1]) and torch.equal(lse[:, :-1], ref_lse[:, :-1])
+    assert torch.isnan(out[:, -1]).all()
+    if np.isnan(value) or cache in ("fp8", "fp4"):  # (an infinite score can be the lowest one)
+        assert torch.isnan(lse[:, -1]).all()
+    assert torch.isfinite(ref.float()).all() and gp.status() == 0
