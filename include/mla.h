@@ -317,6 +317,8 @@ int mla_combine(const mla_dims* dims, const void* W_uv, int batch, int n_q, int 
  *   out          16-byte aligned (MLA_ERR_ALIGNMENT otherwise)
  *   out [batch, n_q, n_heads, d_v] act, lse_out [batch, n_q, n_heads] float32
  *   natural-log softmax denominators (may be NULL)
+ * A row that is not finite makes the results of the queries that see it NaN,
+ * and only those.
  * DeepSeek-V3 dims only (d_c 512, d_rope 64, d_nope = d_v = 128, 64-token
  * pages), bf16 activations, bf16, FP8 or 4-bit cache; MLA_ERR_UNSUPPORTED
  * otherwise.

@@ -80,6 +80,30 @@ __device__ __forceinline__ int seq_keys(const PrefillArgs& a, int b) {
 // ----------------------------------------------------------------------------
 // 1. gather: one warp per key
 // ----------------------------------------------------------------------------
+__device__ __forceinline__ bool finite_bf16x8(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ok = ok && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
+  return ok;
+}
+// Stores a row: c units u0 and u1 (of eight elements) of each lane, k^R unit `lane`
+// of the first lanes.  The K^C and V of a c that is not finite would be NaN, and V
+// meets the probability 0 of every query that does not see the key in one product
+// (0 times NaN).  So such a c is stored as zero, and the NaN in k^R, from where it
+// enters the scores of the queries that do see the key.
+__device__ __forceinline__ void store_row(uint4* c_dst, uint4* kr_dst, int lane, int u0, uint4 x0, int u1, uint4 x1,
+                                          uint4 kr) {
+  const bool ok0 = finite_bf16x8(x0), ok1 = finite_bf16x8(x1);
+  if (!__all_sync(0xffffffffu, ok0 && ok1)) {
+    if (!ok0) x0 = make_uint4(0, 0, 0, 0);
+    if (!ok1) x1 = make_uint4(0, 0, 0, 0);
+    kr = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+  }
+  c_dst[u0] = x0;
+  c_dst[u1] = x1;
+  if (lane < kPDr / 8) kr_dst[lane] = kr;
+}
 __device__ __forceinline__ void gather_row(const PrefillArgs& a, int b, int S, int s, int lane) {
   if (S < 0 || s >= (S + 127) / 128 * 128) return;
   uint4* c_dst = reinterpret_cast<uint4*>(a.C + (size_t)s * kPDc);
@@ -97,11 +121,8 @@ __device__ __forceinline__ void gather_row(const PrefillArgs& a, int b, int S, i
   const uint8_t* pg = a.pool + (size_t)page * a.page_bytes;
   if (a.cache_dtype == MLA_BF16) {
     const uint4* src = reinterpret_cast<const uint4*>(pg + (size_t)row * (kPDc + kPDr) * 2);
-    for (int u = lane; u < (kPDc + kPDr) / 8; u += 32) {
-      const uint4 v = src[u];
-      if (u < kPDc / 8) c_dst[u] = v;
-      else kr_dst[u - kPDc / 8] = v;
-    }
+    const uint4 x0 = src[lane], x1 = src[lane + 32], kr = src[kPDc / 8 + (lane & (kPDr / 8 - 1))];
+    store_row(c_dst, kr_dst, lane, lane, x0, lane + 32, x1, kr);
     return;
   }
   if (a.cache_dtype == MLA_FP4_E2M1) {
@@ -121,10 +142,9 @@ __device__ __forceinline__ void gather_row(const PrefillArgs& a, int b, int S, i
       const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * scale, f.y * scale);
       o[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    c_dst[2 * lane] = make_uint4(o[0], o[1], o[2], o[3]);
-    c_dst[2 * lane + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-    if (lane < kPDr / 8)
-      kr_dst[lane] = reinterpret_cast<const uint4*>(pg + f4.kr_off + (size_t)row * kPDr * 2)[lane];
+    store_row(c_dst, kr_dst, lane, 2 * lane, make_uint4(o[0], o[1], o[2], o[3]), 2 * lane + 1,
+              make_uint4(o[4], o[5], o[6], o[7]),
+              reinterpret_cast<const uint4*>(pg + f4.kr_off + (size_t)row * kPDr * 2)[lane & (kPDr / 8 - 1)]);
     return;
   }
   // FP8: 16 codes per lane, times the scale of their 128-column tile, rounded to bf16
@@ -143,10 +163,9 @@ __device__ __forceinline__ void gather_row(const PrefillArgs& a, int b, int S, i
     o[2 * i] = *reinterpret_cast<const uint32_t*>(&bl);
     o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&bh);
   }
-  c_dst[2 * lane] = make_uint4(o[0], o[1], o[2], o[3]);
-  c_dst[2 * lane + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-  if (lane < kPDr / 8)
-    kr_dst[lane] = reinterpret_cast<const uint4*>(pg + fp.kr_off + (size_t)row * kPDr * 2)[lane];
+  store_row(c_dst, kr_dst, lane, 2 * lane, make_uint4(o[0], o[1], o[2], o[3]), 2 * lane + 1,
+            make_uint4(o[4], o[5], o[6], o[7]),
+            reinterpret_cast<const uint4*>(pg + fp.kr_off + (size_t)row * kPDr * 2)[lane & (kPDr / 8 - 1)]);
 }
 
 __global__ void __launch_bounds__(256) prefill_gather_kernel(const PrefillArgs a, int b) {

@@ -88,3 +88,19 @@ def test_a_hidden_row_does_not_reach_earlier_queries(cache, heads, flags, T, whe
     if np.isnan(value) or cache in ("fp8", "fp4"):  # (an infinite score can be the lowest one)
         assert torch.isnan(lse[:, -1]).all()
     assert torch.isfinite(ref.float()).all() and gp.status() == 0
+
+
+@pytest.mark.parametrize("where", ["c", "kr"])
+@pytest.mark.parametrize("L,T,pos", [(0, 200, 150), (70, 129, 70), (70, 129, 198), (300, 1, 300)])
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp4"])
+def test_prefill_queries_before_the_row_do_not_see_it(cache, L, T, pos, where):
+    cfg, gp = make(cache, 3, 0, T, (L,))
+    append(gp)
+    overwrite(gp, 0, pos, 1.0, where)
+    ref, ref_lse = prefill(cfg, gp)
+    overwrite(gp, 0, pos, float("nan"), where)
+    out, lse = prefill(cfg, gp)
+    n = pos - L  # queries before it
+    assert torch.equal(out[:, :n], ref[:, :n]) and torch.equal(lse[:, :n], ref_lse[:, :n])
+    assert torch.isnan(out[:, n:]).all() and torch.isnan(lse[:, n:]).all()
+    assert torch.isfinite(ref.float()).all() and gp.status() == 0
