@@ -10,7 +10,9 @@
 //   O = sum_k 2^(S_k + e_k - r) (code s)_k,   l = sum_k 2^(S_k - r),
 // S in log2 units, r the row's reference (a running maximum of S + e): code * s
 // is exact in f16 whatever the latent's magnitude, and the probabilities carry
-// the tokens' scales.
+// the tokens' scales.  (l takes a probability times 2^-e, so one that ex2 flushes,
+// below 2^-126, is missing in l: with the scales of a sequence within 2^100 of one
+// another, a key of weight below 2^-26.)
 //
 // Why warp-level MMA and not tcgen05: 16 rows against 420 bytes a key are bound
 // by HBM (35 kFLOP a key), and a tcgen05 operand has to lie in shared memory as

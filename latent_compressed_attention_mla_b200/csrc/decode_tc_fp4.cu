@@ -3,10 +3,11 @@
 // MMAs, an operand ring each for QK and PV fed by converter warps, online softmax
 // from TMEM), with these differences:
 //  * The converters turn e2m1 pairs into f16 by one conversion and one multiply with
-//    the block's scale times the token's (at most six significant bits, so exact
-//    wherever f16 holds the value's range).  A staging slot holds 128 columns,
-//    enough for two units.  k^R and q^R stay bf16: TMA brings the k^R unit straight
-//    into the ring, and its MMAs take the bf16 form.
+//    the block's scale times the token's: exact for token scales from 2^-14 (at most
+//    six significant bits).  Below, f16's subnormals are off by up to 2^-25 in that
+//    scale, times a code of up to 6, and in the product: 7 x 2^-25 in all.  A staging
+//    slot holds 128 columns, enough for two units.  k^R and q^R stay bf16: TMA brings
+//    the k^R unit straight into the ring, and its MMAs take the bf16 form.
 //  * Any head count: the rows (query token, head) of a sequence, r = t * n_heads +
 //    h, form groups of 128, each row with its own causal limit (rows behind the
 //    last are computed and not stored).
@@ -97,14 +98,20 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// 32 e2m1 codes (two blocks of 16 columns) times their scales -> 64 bytes of
-// f16: the 16-byte units u0 ^ e, e = 0..3, of a 128-byte swizzled row.  sc: the
-// blocks' e4m3 scales (low byte first); nan: the f16 pair that a NaN scale
-// becomes (scales are not negative); ts: the token's scale, twice.
-__device__ __forceinline__ void store_e2m1x32(uint8_t* row, uint32_t u0, const uint4& w, uint32_t sc, uint32_t nan,
-                                              uint32_t ts) {
-  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-  const uint32_t s = mul_f16x2(max_f16x2(e4m3x2_to_f16x2(sc), nan), ts), s0 = dup_lo(s), s1 = dup_hi(s);
+// Two blocks' e4m3 scales (low byte first) times the token's scale, as an f16 pair;
+// nan: what a NaN becomes (block scales are not negative).  The product is formed in
+// fp32: a token's scale alone may lie outside f16's range, with a block scale of up to
+// 448 that brings it back, or with 0s where k^R alone makes it large.
+__device__ __forceinline__ uint32_t block_scales(uint32_t sc, uint32_t nan, float ts) {
+  const float2 s = f16x2_to_float2(max_f16x2(e4m3x2_to_f16x2(sc), nan));
+  const __half2 h = __floats2half2_rn(s.x * ts, s.y * ts);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 e2m1 codes (two blocks of 16 columns) times their scales s -> 64 bytes of
+// f16: the 16-byte units u0 ^ e, e = 0..3, of a 128-byte swizzled row.
+__device__ __forceinline__ void store_e2m1x32(uint8_t* row, uint32_t u0, const uint4& w, uint32_t s) {
+  const uint32_t words[4] = {w.x, w.y, w.z, w.w}, s0 = dup_lo(s), s1 = dup_hi(s);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t r[4];
@@ -113,12 +120,6 @@ __device__ __forceinline__ void store_e2m1x32(uint8_t* row, uint32_t u0, const u
     for (int e = 0; e < 4; ++e) r[e] = mul_f16x2(r[e], i < 2 ? s0 : s1);
     *reinterpret_cast<uint4*>(row + ((u0 ^ i) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
   }
-}
-
-// A float as an f16 pair of twice its value.
-__device__ __forceinline__ uint32_t f16x2_of(float x) {
-  const __half2 h = __float2half2_rn(x);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into
@@ -545,25 +546,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L::Threads, 1)
           const uint8_t* const scl = pv ? st_base + stage.slot * st_bytes + kStageBytes : scl_t;
           const uint8_t* const sclr = scl + row * 32 + (pv ? 8 * (int)rank : 8 * c);
           const uint8_t* const tsr = scl + 2048 + row * 4;
-          uint2 g0 = *reinterpret_cast<const uint2*>(sclr), g1 = *reinterpret_cast<const uint2*>(sclr + scl_g);
-          uint32_t ts[2] = {f16x2_of(*reinterpret_cast<const float*>(tsr)),
-                            f16x2_of(*reinterpret_cast<const float*>(tsr + ts_a))};
-          if (!live) {  // zero scales: the codes of rows past the end may be anything
-            g0 = g1 = make_uint2(0, 0);
-            ts[0] = ts[1] = 0;
-          }
-          const uint32_t m01 = pv ? g0.y : g1.x, m10 = pv ? g1.x : g0.y;  // (unit, half)
+          const uint2 g0 = *reinterpret_cast<const uint2*>(sclr), g1 = *reinterpret_cast<const uint2*>(sclr + scl_g);
+          const float t0 = *reinterpret_cast<const float*>(tsr), t1 = *reinterpret_cast<const float*>(tsr + ts_a);
+          // the thread's two blocks of each (unit, half)
+          uint32_t s00 = block_scales(g0.x >> (16 * q), nan, t0);
+          uint32_t s01 = block_scales((pv ? g0.y : g1.x) >> (16 * q), nan, t1);
+          uint32_t s10 = block_scales((pv ? g1.x : g0.y) >> (16 * q), nan, t0);
+          uint32_t s11 = block_scales(g1.y >> (16 * q), nan, t1);
+          if (!live) s00 = s01 = s10 = s11 = 0;  // rows past the end: their bytes may be anything
 #pragma unroll 1
           for (int u = 0; u < 2; ++u) {
             const uint4 v[2] = {*reinterpret_cast<const uint4*>(src + (pv ? u * 4096 + x0 : u ? x1 : x0)),
                                 *reinterpret_cast<const uint4*>(src + (pv ? u * 4096 + x1 : 4096 + (u ? x1 : x0)))};
-            const uint32_t sc[2] = {u ? m10 : g0.x, u ? g1.y : m01};
+            const uint32_t sc[2] = {u ? s10 : s00, u ? s11 : s01};
             ok = mbar_wait(un_empty + 8 * unit.slot, unit.phase ^ 1, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);  // the warp leaves together
             if (!ok) break;
             uint8_t* const dst = ring + unit.slot * kUnitBytes;
 #pragma unroll
-            for (int a = 0; a < 2; ++a) store_e2m1x32(dst + a * 8192, u0, v[a], sc[a] >> (16 * q), nan, ts[a]);
+            for (int a = 0; a < 2; ++a) store_e2m1x32(dst + a * 8192, u0, v[a], sc[a]);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(un_full + 8 * unit.slot);
