@@ -9,8 +9,8 @@ the absorbed form, itself pinned to the explicit one, for all heads of long
 sequences).
 
 A problem may scale chosen history rows by powers of two ("row gains"), the
-same on both sides: the latent c of a bf16 / fp32 row, or the per-tile scales
-of an FP8 row.  That multiplies the latent part of those keys' scores exactly
+same on both sides: the latent c of a bf16 / fp32 row, the per-tile scales of
+an FP8 row, or the token scale of a 4-bit row.  That multiplies the latent part of those keys' scores exactly
 (no rounding on either side) and is how the tests reach wide logit ranges."""
 from __future__ import annotations
 
@@ -31,10 +31,10 @@ def _check_gains(g: np.ndarray):
 
 def apply_row_gains(rows: dict, gains: np.ndarray) -> dict:
     """rows as generated (torch tensors of one sequence's consecutive positions),
-    gains float [n] powers of two: latent c (or FP8 scales) of row i times gains[i]."""
+    gains float [n] powers of two: latent c (or FP8 scales, or 4-bit token scale) of row i times gains[i]."""
     _check_gains(gains)
     out = dict(rows)
-    key = "scales" if "codes" in rows else "c"
+    key = "ts" if "ts" in rows else "scales" if "codes" in rows else "c"
     x = rows[key]
     g = torch.from_numpy(np.asarray(gains, dtype=np.float32)).to(x.device)
     out[key] = (x.float() * g[:, None]).to(x.dtype)
@@ -103,7 +103,10 @@ class OracleProblem:
         rows = W.history_rows(self.cfg, b, 0, L, "cpu")
         if self.row_gain is not None:
             rows = apply_row_gains(rows, self.row_gain(b, np.arange(L)))
-        if "codes" in rows:
+        if "ts" in rows:
+            rows = {"codes": rows["codes"].numpy(), "scales": rows["scales"].numpy(),
+                    "ts": rows["ts"].double().numpy(), "kr": rows["kr"].double().numpy()}
+        elif "codes" in rows:
             rows = {"codes": rows["codes"].numpy(), "scales": rows["scales"].double().numpy(),
                     "kr": rows["kr"].double().numpy()}
         else:
