@@ -398,6 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L::Threads, 1)
         const bool resc = __any_sync(0xffffffffu, rescale);
         if (resc) ok = wait_pv_rescale();
         tc_fence_before();
+        __syncwarp();  // lane 0 arrives for all: every lane's part of O is rescaled
         if (half == 1 && lane == 0) mbar_arrive_cluster(leader_bar(L::P_FULL));
         if (g >= 1 && ok && !resc)
           ok = __all_sync(0xffffffffu, mbar_wait(bar(half ? L::O_DONE : L::P_FREE), (g - 1) & 1, abort_flag, p.status));
