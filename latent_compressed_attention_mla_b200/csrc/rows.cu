@@ -143,7 +143,9 @@ __device__ __forceinline__ void unpack16(const Raw16<T>& r, float (&x)[16]) {
 // r = 1 / sqrt(mean(c^2) + eps).  The quantisers cut y into codes whose
 // borders bf16 inputs meet exactly, so y is the correctly rounded fp32 value up to
 // an error of 2^-48: the sum and r are formed in 64 bits, c w as a product and
-// its remainder, r as the sum of two floats.
+// its remainder, r as the sum of two floats.  Where the mean square lies beyond
+// 2^+-100, a power of two goes from r to c first, so that neither c w (beyond fp32's
+// range) nor the remainders (subnormal) lose anything.
 template <typename T, int NB, bool VEC, bool AHEAD>
 __device__ __forceinline__ void rms_norm(const RowsArgs& a, int lane, int nb, const Raw16<T>& w0, float (&x)[NB][16]) {
   double ss = 0.0;
@@ -156,7 +158,16 @@ __device__ __forceinline__ void rms_norm(const RowsArgs& a, int lane, int nb, co
     }
 #pragma unroll
   for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const double r = rsqrt(fma(ss, a.inv_dc, a.norm_eps));
+  const double ms = fma(ss, a.inv_dc, a.norm_eps);  // the same in every lane
+  double r = rsqrt(ms);
+  if (ms > 0x1p100 || ms < 0x1p-100) {
+    const float f = ms > 1.0 ? 0x1p-50f : 0x1p50f;
+    r *= ms > 1.0 ? 0x1p50 : 0x1p-50;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[j][e] *= f;
+  }
   const float r_hi = (float)r, r_lo = (float)(r - (double)r_hi);
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
