@@ -428,7 +428,7 @@ struct CacheUnit<MLA_FP8_E4M3, VEC> {
   float s;
   __device__ __forceinline__ void load(const ReadArgs& a, const uint8_t* pg, int prow, int b) {
     w = *reinterpret_cast<const uint2*>(pg + (size_t)prow * a.d_c + 8 * b);
-    s = reinterpret_cast<const float*>(pg + fp8_page(a.page_size, a.d_c, a.d_rope).sc_off)[prow * (a.d_c / 128) + b / 16];
+    s = reinterpret_cast<const float*>(pg + fp8_page(a.page_size, a.d_c, a.d_rope).sc_off)[(size_t)prow * (a.d_c / 128) + b / 16];
   }
   __device__ __forceinline__ void values(float (&y)[8]) const {
 #pragma unroll
@@ -442,8 +442,8 @@ struct CacheUnit<MLA_FP4_E2M1, VEC> {
   uint8_t sc;
   __device__ __forceinline__ void load(const ReadArgs& a, const uint8_t* pg, int prow, int b) {
     const Fp4Page f4 = fp4_page(a.page_size, a.d_c, a.d_rope);
-    w = *reinterpret_cast<const uint32_t*>(pg + prow * (a.d_c / 2) + 4 * b);
-    sc = pg[f4.sc_off + prow * (a.d_c / 16) + b / 2];
+    w = *reinterpret_cast<const uint32_t*>(pg + (size_t)prow * (a.d_c / 2) + 4 * b);
+    sc = pg[f4.sc_off + (size_t)prow * (a.d_c / 16) + b / 2];
     ts = reinterpret_cast<const float*>(pg + f4.ts_off)[prow];
   }
   __device__ __forceinline__ void values(float (&y)[8]) const {

@@ -7,6 +7,7 @@ import torch
 
 from latent_compressed_attention_mla_b200 import binding as B
 from latent_compressed_attention_mla_b200 import workloads as W
+from latent_compressed_attention_mla_b200.paged_cache import PagedLatentCache
 from tests.test_gpu_rows import TYPES, Rows
 
 pytestmark = pytest.mark.gpu
@@ -24,3 +25,28 @@ def test_norm_of_very_large_and_small_rows(act, cache, d_c, d_rope, size, eps):
     r.append(True, eps)
     r.check(True, float(np.float32(eps)))  # the value that the fp32 argument carries
     assert torch.isfinite(r.kv).all() and B.mla_get_status() == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "fp4"])
+def test_rows_of_a_page_beyond_32_bits_of_bytes(cache):
+    """A page of 2^23 + 64 tokens (one page a sequence): the last rows lie more than
+    2^31 bytes into it."""
+    size, d_c = (1 << 23) + 64, 512
+    pos = torch.tensor([0, 1, size // 2, size - 65, size - 64, size - 2, size - 1], dtype=torch.int32).cuda()
+    n = len(pos)
+    c = W.normal(78, 1, n * d_c).view(n, d_c).to(torch.bfloat16).cuda()
+    kr = W.normal(78, 2, n * 2).view(n, 2).to(torch.bfloat16).cuda()
+    seq = torch.zeros(n, dtype=torch.int32).cuda()
+
+    def through(page, at):
+        dims = B.make_dims(8, d_c, 2, 128, 128, 512, page_size=page, act="bf16", cache=cache)
+        pool = PagedLatentCache(dims, 1, "cuda", fill=0)
+        table = torch.zeros(1, 1, dtype=torch.int32).cuda()
+        pool.append(c, kr, seq, at, table)
+        got = pool.values(seq, at, table)
+        return got[0], got[1], pool.views()["kr"][0, at.long()]
+
+    big, small = through(size, pos), through(n, torch.arange(n, dtype=torch.int32).cuda())
+    assert torch.equal(big[0], small[0]) and big[0].abs().sum() > 0
+    assert torch.equal(big[1], big[2])
+    assert B.mla_get_status() == 0
