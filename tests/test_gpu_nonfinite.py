@@ -104,3 +104,22 @@ def test_prefill_queries_before_the_row_do_not_see_it(cache, L, T, pos, where):
     assert torch.equal(out[:, :n], ref[:, :n]) and torch.equal(lse[:, :n], ref_lse[:, :n])
     assert torch.isnan(out[:, n:]).all() and torch.isnan(lse[:, n:]).all()
     assert torch.isfinite(ref.float()).all() and gp.status() == 0
+
+
+@pytest.mark.parametrize("cache,heads", [("bf16", 128), ("fp8", 128), ("fp4", 128), ("fp4", 40), ("fp4", 8)])
+@pytest.mark.parametrize("batch,T", [(12, 2), (40, 2), (40, 1)])
+def test_rows_in_a_large_batch(cache, heads, batch, T):
+    """Every block size of the combine: only the sequences with such a row are NaN."""
+    cfg, gp = make(cache, heads, 0, T, [60 + 37 * i for i in range(batch)])
+    out, lse = gp.run()
+    ref, ref_lse = out.clone(), lse.clone()
+    bad = [1, 7, batch - 1]
+    for b in bad:
+        overwrite(gp, b, 20 * b, float("nan"), "kr" if b == 7 else "c")
+    out, lse = gp.attend_only()
+    for b in range(batch):
+        if b in bad:
+            assert torch.isnan(out[b]).all() and torch.isnan(lse[b]).all()
+        else:
+            assert torch.equal(out[b], ref[b]) and torch.equal(lse[b], ref_lse[b])
+    assert torch.isfinite(ref.float()).all() and gp.status() == 0
