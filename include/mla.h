@@ -200,8 +200,8 @@ int mla_append_latent(const mla_dims* dims, const void* h, int n_tokens,
  * store alone, with the RMSNorm of the latent that models put in between.
  *   c~_n  = c_n, or with norm_weight  norm_weight * c_n / sqrt(mean(c_n^2) + norm_eps)
  *   k^R_n = RoPE(k_rope_n, pos[n])   (as mla_append_latent)
- * and store [c~_n | k^R_n] at (seq_idx[n], pos[n]), rounded once to the cache
- * type (the quantisers of the layouts above, from the fp32 value of c~).
+ * and store [c~_n | k^R_n] at (seq_idx[n], pos[n]), rounded to the cache type
+ * from the fp32 value of c~ (the quantisers of the layouts above).
  *   c           n_tokens rows of d_c act elements, c_stride elements apart
  *   k_rope      n_tokens rows of d_rope act elements, k_stride elements apart,
  *               not rotated; may be NULL when d_rope is 0

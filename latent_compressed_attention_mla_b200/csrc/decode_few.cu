@@ -39,14 +39,17 @@
 // independent streams of conversions and MMAs (two warps a scheduler are too
 // few to hide one stream's latencies; P is double-buffered).
 //
-// Measured (16 heads): 128 sequences of 16,385 keys 377 us, 2.4 TB/s of cache rows;
-// 8 of 131,073 202 us.  HBM would allow 135 and 68; loads alone take 148.  Bound by
-// the math pipes: each code becomes f16 twice (scores, values), and per 128 keys a
+// Measured (16 heads, this kernel's span on the device): 128 sequences of 16,385 keys
+// 360 us, 2.4 TB/s of cache rows; 8 of 131,073 188 us.  HBM would allow 135 and 68;
+// loads alone take 148.  Each code becomes f16 twice (scores, values): per 128 keys a
 // scheduler issues 272 MMAs (8.6 cycles each), 512 conversions of two codes (2) and
-// 512 multiplies.  Twice the warps do not help: sixteen with half the work each
-// 382 us, two teams of eight on alternate pages, one's softmax beside the other's
-// products, 394 us.  On the way: one phase for scores, one for values 499 us; query
-// fragments in registers, not shared memory 412 us.
+// 512 multiplies, 3,900 cycles end to end of the 6,400 that a tile takes.  The rest,
+// some 40%, is latency between the phases: the exchange of the score halves, the
+// softmax and the barrier run with the tensor and conversion pipes (30% and 36%
+// busy) idle.  Twice the warps with half the work each (+1%) and two teams of eight
+// on alternate pages, one's softmax beside the other's products (+4%), did not hide
+// it.  On the way: one phase for scores, one for values +32%; query fragments in
+// registers, not shared memory +9%.
 #include <cuda.h>
 
 #include <cstring>

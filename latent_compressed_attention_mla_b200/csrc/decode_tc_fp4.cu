@@ -16,13 +16,17 @@
 //  * Roles: warps 0-3 softmax and epilogue, 4 TMEM allocation and (leader) QK issue,
 //    5 (leader) PV issue, 6 / 7 TMA for Q and QK / PV data, 8-11 / 12-15 converters
 //    of QK / PV units.
-// Measured: 128 heads, 128 sequences of 16,386 keys with two query tokens 1,201 us
-// (970 TFLOP/s; CUDA cores 410 ms), 64 ragged sequences of up to 32,769 keys 346
-// us (64 heads: 315 us).  Bound by the converters: a tile of 256 keys takes 5.5
-// us, of which the QK converters are busy 5.1 (shared memory 63% busy, tensor pipe
-// 38%).  On the way: k^R converted like the codes 1.475 ms, P handed over whole
-// 1.412, a loop unrolled over the units 1.69 (instruction cache; the producers' loops
-// alone, unrolled, 1.255: hence their unroll 1).
+// Measured (this kernel's span on the device): 128 heads, 128 sequences of 16,386 keys
+// with two query tokens 1,209 us (963 TFLOP/s; CUDA cores 410 ms), 64 ragged sequences
+// of up to 32,769 keys 349 us (64 heads: 312 us).  A tile of 256 keys takes 5.5 us, of
+// which the QK converters are busy 5.1, but no unit is at its limit (shared memory
+// 63%, tensor pipe and ALU 38%): each scheduler has one warp of a ring's four, whose
+// waits, loads, conversions and stores follow one another, and that chain's latency is
+// the time.  The bf16 cache, which needs no conversion, takes 1,071 us on the large
+// batch: with all heads on one GPU the 4-bit cache saves memory, not time.  On the
+// way: k^R converted like the codes 1.475 ms, P handed over whole 1.412, a loop
+// unrolled over the units 1.69 (instruction cache; the producers' loops alone,
+// unrolled, 1.255: hence their unroll 1).
 //
 // A kernel of its own and not a variant of decode_tc.cu's: in one template, with this
 // one's order of roles, the FP8 variant took 1,739 us for 1,630 on the same sequences.

@@ -15,12 +15,13 @@
 // three shuffles, the norm's sum and the token's maximum five.  Every input
 // byte is read once and every output byte written once (V3 dims, bf16 in, 4-bit
 // out: 1,152 + 420 bytes a token).  Measured on 32,792 tokens, where HBM would
-// allow 7.9 us each way: append with norm 26.4 us (2.0 TB/s), read 11.2 us (4.6
-// TB/s).  The append is bound by issue (65% of the slots; 600 instructions a
-// token: 64-bit norm, angles, quotients), so its warps load the next row while they
-// work on one (30 -> 26.4); the read by latency, so a warp takes four tokens at a
-// time and stores whole sectors (18 -> 11.2).  Calls of up to some thousand tokens
-// take 3 to 7 us on the device, less than their launch costs the host.
+// allow 7.9 us each way: append with norm 26.6 us (2.0 TB/s), without 20.4, read 10.9
+// (4.7 TB/s).  To an 8-bit cache (floor 9.1) 29.4, 22.5 and 11.0 us, to a bf16 one
+// (11.5) 19.3, 13.9 and 12.9.  The append is bound by issue (65% of the slots; 600
+// instructions a token: 64-bit norm, angles, quotients), so its warps load the next
+// row while they work on one (30 -> 26 us); the read by latency, so a warp takes four
+// tokens at a time and stores whole sectors (18 -> 11).  Calls of up to some thousand
+// tokens take 3 to 7 us on the device, less than their launch costs the host.
 #include <math.h>
 
 #include "mla_internal.cuh"
