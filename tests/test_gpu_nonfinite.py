@@ -123,3 +123,22 @@ def test_rows_in_a_large_batch(cache, heads, batch, T):
         else:
             assert torch.equal(out[b], ref[b]) and torch.equal(lse[b], ref_lse[b])
     assert torch.isfinite(ref.float()).all() and gp.status() == 0
+
+
+@pytest.mark.parametrize("heads,T,flags", [(1, 16, 0), (2, 8, 0), (16, 8, 0), (20, 5, 0), (128, 3, 0), (128, 9, 0),
+                                           (4, 16, B.MLA_FLAG_FORCE_SIMT)])
+@pytest.mark.parametrize("splits", [0, 1])
+def test_a_row_among_many_new_tokens(heads, T, flags, splits):
+    """One of the new tokens, which may lie in two pages or two tiles, is not finite."""
+    cfg, gp = make("fp4", heads, flags, T, (0, 50, 60, 120, 250), splits)
+    out, lse = gp.run()
+    ref, ref_lse = out.clone(), lse.clone()
+    assert torch.isfinite(ref.float()).all()
+    for k in (1, T // 2, T - 1):
+        gp.run()  # the rows as they were
+        for b in range(cfg.B):
+            overwrite(gp, b, int(cfg.L[b]) + k, float("nan"), "c")
+        out, lse = gp.attend_only()
+        assert torch.equal(out[:, :k], ref[:, :k]) and torch.equal(lse[:, :k], ref_lse[:, :k])
+        assert torch.isnan(out[:, k:]).all() and torch.isnan(lse[:, k:]).all()
+    assert gp.status() == 0
