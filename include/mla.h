@@ -263,9 +263,9 @@ int mla_read_rows(const mla_dims* dims, const void* cache_pool, int num_pages,
  * probabilities as f16 (|q~| up to 65504).  The tcgen05 kernel (path 1) holds the
  * latent as f16 too, |c| up to 64512.  Of a 4-bit cache it takes the rows exactly
  * whose token scale is 2^-14 or more (a, above, 2^-9 or more), and others to an
- * absolute 2^-22.  Of an FP8 cache it holds the tiles' scales as f16 (relative
- * 2^-12; an absolute 2^-16 of the latent where a tile's largest |c| is below 2^-5),
- * and k^R, up to 65504.  The few-row kernel (path 2) takes 4-bit rows exactly at
+ * absolute 2^-22.  Of an FP8 cache it rounds the tiles' scales to f16 (relative
+ * 2^-12; an absolute 2^-16 of the latent where a tile's largest |c| is below 2^-5)
+ * and their products with the codes again, and k^R, up to 65504.  The few-row kernel (path 2) takes 4-bit rows exactly at
  * any token scale, as long as those of a sequence lie within 2^100 of one another.
  * A visible row that is not finite makes the query's scores and results NaN
  * (out and lse_out of mla_combine), whatever the splits.
