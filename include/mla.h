@@ -265,8 +265,9 @@ int mla_read_rows(const mla_dims* dims, const void* cache_pool, int num_pages,
  * whose token scale is 2^-14 or more (a, above, 2^-9 or more), and others to an
  * absolute 2^-22.  Of an FP8 cache it rounds the tiles' scales to f16 (relative
  * 2^-12; an absolute 2^-16 of the latent where a tile's largest |c| is below 2^-5)
- * and their products with the codes again, and k^R, up to 65504.  The few-row kernel (path 2) takes 4-bit rows exactly at
- * any token scale, as long as those of a sequence lie within 2^100 of one another.
+ * and their products with the codes again, and k^R, up to 65504.  The few-row
+ * kernel (path 2) takes 4-bit rows exactly at any token scale, as long as those of
+ * a sequence lie within 2^100 of one another.
  * A visible row that is not finite makes the query's scores and results NaN
  * (out and lse_out of mla_combine), whatever the splits.
  * The workspace is consumed by the next mla_combine with the same dims, batch,
